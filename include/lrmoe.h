@@ -449,6 +449,174 @@ lrmoe_status lrmoe_grouped_backward_gate_up_timed(
     const void* x_c, const void* W, float* dW, float* dx, void* workspace, size_t ws_bytes,
     void* stream, const lrmoe_timing* timing);
 
+/* ------------------------------------------------------------------------
+ * The forward side: what produces the pairs, projection inputs and
+ * pre-activations that the backward above reads, and the gradients of the
+ * steps around it.
+ *
+ *   gate      router logits -> expert ids and weights of each token
+ *   sort      ids -> pairs in expert order (counts, segments, rows, alpha)
+ *   dispatch  token rows -> pair rows          (gradient: sum over a token)
+ *   product   z_u = W_e x_u + bias, y_u = act(z_u) + residual, per expert
+ *                                              (gradient of the epilogue; the
+ *             product's own is lrmoe_grouped_backward with quotas = counts)
+ *   combine   pair rows -> weighted token rows (gradient: rows and weights)
+ *
+ * The rules above hold here too (dense row-major, device pointers 16-byte
+ * aligned, row lengths multiples of 8 (bf16) or 4 (float32), outputs not
+ * aliasing inputs, nothing allocated, errors before any launch).  Expert
+ * counts and segments stay on the device: nothing visits the host between
+ * these calls, so a whole layer can be captured in a graph.  A graph that is
+ * replayed beside other calls needs a workspace of its own.
+ * ------------------------------------------------------------------------ */
+
+#define LRMOE_MAX_GATE_EXPERTS 1024 /* experts of a router row               */
+#define LRMOE_MAX_TOPK 64           /* slots of a token                      */
+
+typedef enum { LRMOE_GATE_SOFTMAX = 0, LRMOE_GATE_SIGMOID = 1 } lrmoe_gate_score;
+
+typedef struct {
+  int64_t T;       /* tokens, T * K < 2^31                                   */
+  int32_t E;       /* experts of a row, 1 .. LRMOE_MAX_GATE_EXPERTS          */
+  int32_t K;       /* slots, 1 .. min(E, LRMOE_MAX_TOPK)                     */
+  int32_t dtype;   /* lrmoe_dtype of the logits                              */
+  int32_t score;   /* lrmoe_gate_score                                       */
+  int32_t renorm;  /* non-zero: weights of the chosen experts sum to scale   */
+  float scale;     /* factor on every weight                                 */
+} lrmoe_gate;
+
+/* Top-k gate.  logits [T, E] (any E: a row need not be 16-byte aligned).
+ * Selection key of expert e: its logit x_e, or with select_bias (float32 [E],
+ * sigmoid score only, else LRMOE_ERR_INVALID) sigmoid(x_e) + select_bias[e]
+ * in float64.  The K largest keys, best first, ties to the lower expert:
+ *   ids      int32 [T, K]
+ *   weights  float32 [T, K]: scale * the score of the chosen experts, softmax
+ *            over the row (SOFTMAX) or sigmoid (SIGMOID); with renorm
+ *            normalised over the chosen ones instead.  The bias enters the
+ *            selection only.
+ * A logit of -inf or NaN masks its expert (+inf counts as the largest finite
+ * value); so does a NaN or -inf key.  Where fewer than K experts are left,
+ * the last slots hold id -1 and weight 0. */
+lrmoe_status lrmoe_gate_topk(const lrmoe_gate* gt, const void* logits, const float* select_bias,
+                             int32_t* ids, float* weights, void* stream);
+
+/* Gradient of the gate's weights: dlogits [T, E] in the logits' type, fully
+ * overwritten, from dweights float32 [T, K] at the ids of lrmoe_gate_topk (or
+ * any others: a slot with an id outside 0..E-1 carries nothing, and an
+ * expert standing in two slots gets the sum of both).  The selection itself
+ * has no gradient. */
+lrmoe_status lrmoe_gate_topk_backward(const lrmoe_gate* gt, const void* logits,
+                                      const int32_t* ids, const float* dweights, void* dlogits,
+                                      void* stream);
+
+/* Workspace bytes of lrmoe_route_sort (0 for few pairs). */
+lrmoe_status lrmoe_route_sort_workspace(int64_t T, int32_t K, int32_t E, size_t* bytes_out);
+
+/* Stable sort of the T * K slots by expert.  ids int32 [T, K], local expert
+ * indices; a slot whose id is outside 0..E-1 is routed elsewhere.  With P
+ * the slots routed here (= seg_offsets[E], known on the device only):
+ *   counts       int64 [E]
+ *   seg_offsets  int32 [E + 1]
+ *   row_index    int32 [T * K]: token of each pair in expert order, pairs of
+ *                one expert in ascending slot order; -1 behind the last pair
+ *   pos          int32 [T, K]: each slot's place in that order, -1 elsewhere
+ *   alpha        float32 [T * K] or NULL: weights (float32 [T, K]) in that
+ *                order, 0 behind the last pair
+ * T * K < 2^31; E <= LRMOE_MAX_EXPERTS; K <= LRMOE_MAX_TOPK. */
+lrmoe_status lrmoe_route_sort(int64_t T, int32_t K, int32_t E, const int32_t* ids,
+                              const float* weights, int64_t* counts, int32_t* seg_offsets,
+                              int32_t* row_index, int32_t* pos, float* alpha, void* workspace,
+                              size_t ws_bytes, void* stream);
+
+/* xp[pos[t, k]] = x[t]: x [T, D], xp [P, D] of one type.  P is the capacity
+ * of xp: a place outside 0..P-1 is skipped, and rows no slot names are left
+ * as they were.  (lrmoe_grouped_forward can read x through row_index
+ * instead, without this copy.) */
+lrmoe_status lrmoe_dispatch(int32_t dtype, int64_t T, int32_t K, int32_t D, int64_t P,
+                            const void* x, const int32_t* pos, void* xp, void* stream);
+
+/* dx[t] = sum_k dxp[pos[t, k]] (float32 sum in ascending k, one rounding):
+ * dxp [P, D] of type dtype (float32 for lrmoe_grouped_backward's dphi), dx
+ * [T, D] of type out_dtype, fully overwritten. */
+lrmoe_status lrmoe_dispatch_backward(int32_t dtype, int32_t out_dtype, int64_t T, int32_t K,
+                                     int32_t D, int64_t P, const void* dxp, const int32_t* pos,
+                                     void* dx, void* stream);
+
+/* y[t] = residual[t] + sum_k weights[t, k] * yp[pos[t, k]] (float32, one
+ * rounding): yp [P, D], y [T, D], residual [T, D] or NULL, of one type;
+ * weights float32 [T, K].  A token without a place gets its residual, or 0. */
+lrmoe_status lrmoe_combine(int32_t dtype, int64_t T, int32_t K, int32_t D, int64_t P,
+                           const void* yp, const int32_t* pos, const float* weights,
+                           const void* residual, void* y, void* stream);
+
+/* Gradient of lrmoe_combine from dy [T, D]: dyp[pos[t, k]] = weights[t, k] *
+ * dy[t] ([P, D]; rows no slot names are left as they were) and dweights
+ * float32 [T, K] = <dy[t], yp[pos[t, k]]> (0 without a place).  (The
+ * residual's gradient is dy.)  Two slots must not share a place. */
+lrmoe_status lrmoe_combine_backward(int32_t dtype, int64_t T, int32_t K, int32_t D, int64_t P,
+                                    const void* dy, const void* yp, const int32_t* pos,
+                                    const float* weights, void* dyp, float* dweights,
+                                    void* stream);
+
+/* Activation of the grouped product's epilogue.  GELU is the exact one (with
+ * the error function).  SWIGLU: the first half of W_e's rows gives the gate
+ * a, the second half b; y = SiLU(a) * b. */
+typedef enum {
+  LRMOE_ACT_NONE = 0,
+  LRMOE_ACT_RELU = 1,
+  LRMOE_ACT_SILU = 2,
+  LRMOE_ACT_GELU = 3,
+  LRMOE_ACT_SWIGLU = 4
+} lrmoe_act;
+
+typedef struct {
+  int32_t E;      /* experts, 1 .. LRMOE_MAX_EXPERTS                         */
+  int32_t dtype;  /* storage of x, W, bias, residual, y and pre-activations  */
+  int64_t P;      /* pair rows (capacity), 0 <= P < 2^31                     */
+  int64_t T;      /* rows of x (T == P without a row_index)                  */
+  int32_t d_out;  /* rows of W_e (2 F for SWIGLU)                            */
+  int32_t d_in;   /* columns of W_e                                          */
+  int32_t act;    /* lrmoe_act                                               */
+} lrmoe_forward;
+
+/* y_u = act(W_e x_{row(u)} + bias_e) + residual_u for the pairs u of expert
+ * e, seg_offsets[e] <= u < seg_offsets[e + 1] (device int32 [E + 1],
+ * ascending, at most P; rows behind the last segment are left as they were).
+ * F = d_out, or d_out / 2 for SWIGLU.
+ *   row_index  int32 [P] device or NULL (row u): an index outside 0..T-1
+ *              reads a zero row
+ *   x [T, d_in], W [E, d_out, d_in], bias [E, d_out] or NULL,
+ *   residual [P, F] or NULL, y [P, F]
+ *   pre_a [P, F] (and pre_b, both or none, for SWIGLU): W x + bias before the
+ *              activation, in the layout lrmoe_act_backward and
+ *              lrmoe_grouped_backward_glu read; NULL: not stored
+ * One segment (E = 1) is the dense product of a shared expert.  float32
+ * accumulation and epilogue, one rounding; float32 storage multiplies in
+ * float32. */
+lrmoe_status lrmoe_grouped_forward(const lrmoe_forward* fw, const int32_t* seg_offsets,
+                                   const int32_t* row_index, const void* x, const void* W,
+                                   const void* bias, const void* residual, void* y, void* pre_a,
+                                   void* pre_b, void* stream);
+
+/* Workspace bytes of lrmoe_act_backward when dbias is asked for. */
+lrmoe_status lrmoe_act_backward_workspace(const lrmoe_forward* fw, size_t* bytes_out);
+
+/* Gradient of the epilogue, from dy [P, F]:
+ *   dz     [P, d_out] of type dz_dtype (the storage type, or float32 for the
+ *          unrounded hand-off to lrmoe_grouped_backward_gate_up): dy act'(a),
+ *          for SWIGLU [dy b SiLU'(a) | dy SiLU(a)]; rows behind the last
+ *          segment are left as they were
+ *   dbias  float32 [E, d_out] or NULL: sum of the unrounded dz over the
+ *          expert's rows (0 without rows), in an order that does not depend
+ *          on timing
+ * pre_a (and pre_b for SWIGLU) as stored by lrmoe_grouped_forward; pre_a is
+ * not read for LRMOE_ACT_NONE.  The residual's gradient is dy.  fw's T and
+ * d_in are checked but not used.  workspace: NULL without dbias. */
+lrmoe_status lrmoe_act_backward(const lrmoe_forward* fw, int32_t dz_dtype,
+                                const int32_t* seg_offsets, const void* dy, const void* pre_a,
+                                const void* pre_b, void* dz, float* dbias, void* workspace,
+                                size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,7 +16,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblrmoe.so")
-SOURCES = ["api.cpp", "score_select.hip", "gather.hip", "grouped_gemm.hip", "plan_quota.hip"]
+SOURCES = ["api.cpp", "score_select.hip", "gather.hip", "grouped_gemm.hip", "plan_quota.hip",
+           "api_forward.cpp", "gate.hip", "route.hip", "grouped_forward.hip", "act_backward.hip"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,233 @@
+// Gradient of the grouped product's epilogue (bias and activation), ahead of
+// the product's own gradients:
+//
+//   dz_u = dy_u act'(a_u)                          (a: saved pre-activations)
+//   SwiGLU: dz_u = [ dy_u b_u SiLU'(a_u) | dy_u SiLU(a_u) ]
+//   dbias_e = sum over the expert's rows of dz_u   (before dz's rounding)
+//
+//   SiLU'(a) = s (1 + a (1 - s)), s = sigmoid(a)
+//   GELU'(a) = Phi(a) + a phi(a)
+//
+// Memory bound: dy, a (and b) are read once, dz written once.  A workgroup
+// takes a run of kRows rows of one expert and 64 * N columns; its four waves
+// take every fourth row and keep the column sums in registers, which meet in
+// LDS and go to the workspace, one row of sums for each run.  A second kernel
+// adds an expert's runs in order, so the sums do not depend on timing.
+#include "forward.h"
+
+namespace lrmoe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = 4;
+constexpr int kRows = 64;
+
+// Runs of an expert with n rows.
+__host__ __device__ inline int64_t runs_of(int64_t n) { return (n + kRows - 1) / kRows; }
+// Bound of the runs of all experts.
+int64_t max_runs(int64_t P, int E) { return P / kRows + (P < E ? P : E); }
+
+// Segment e of the (untrusted) device offsets, inside [0, P].
+__device__ __forceinline__ void segment(const int32_t* seg, int e, int64_t P, int64_t& lo,
+                                        int64_t& hi) {
+  lo = seg[e] < 0 ? 0 : seg[e] > P ? P : seg[e];
+  hi = seg[e + 1] < lo ? lo : seg[e + 1] > P ? P : seg[e + 1];
+}
+
+// Expert of run r and the run's number inside it, or false past the last run.
+// Every wave finds it for itself: lane l looks at experts 4 l .. 4 l + 3.
+__device__ __forceinline__ bool find_run(const int32_t* seg, int E, int64_t P, int64_t r, int& e,
+                                         int64_t& sub) {
+  const int lane = threadIdx.x & 63;
+  int64_t n[4], sum = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    n[j] = 0;
+    if (4 * lane + j < E) {
+      int64_t lo, hi;
+      segment(seg, 4 * lane + j, P, lo, hi);
+      n[j] = runs_of(hi - lo);
+    }
+    sum += n[j];
+  }
+  int64_t end = sum;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const int64_t o = __shfl_up(end, m, 64);
+    if (lane >= m) end += o;
+  }
+  const unsigned long long past = __ballot(end > r);
+  if (past == 0) return false;
+  const int owner = __ffsll(past) - 1;
+  int64_t at = r - (end - sum);   // meant for the owner lane
+  int j = 0;
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    if (j == i && at >= n[i]) {
+      at -= n[i];
+      j = i + 1;
+    }
+  e = __builtin_amdgcn_readfirstlane(__shfl(4 * lane + j, owner, 64));
+  sub = __shfl(at, owner, 64);
+  return true;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_grad(float a) {
+  if constexpr (ACT == LRMOE_ACT_RELU) return a > 0.f ? 1.f : 0.f;
+  if constexpr (ACT == LRMOE_ACT_SILU || ACT == LRMOE_ACT_SWIGLU) {
+    const float s = sigmoid_f32(a);
+    return s * (1.f + a * (1.f - s));
+  }
+  if constexpr (ACT == LRMOE_ACT_GELU)
+    return 0.5f * (1.f + erff(a * 0.70710678f)) + a * (0.39894228f * expf(-0.5f * a * a));
+  return 1.f;
+}
+
+template <typename T, typename TO, int N, int ACT>
+__global__ __launch_bounds__(kThreads) void act_backward_kernel(
+    const int32_t* __restrict__ seg, const T* __restrict__ dy, const T* __restrict__ pa,
+    const T* __restrict__ pb, int64_t P, int E, int F, TO* __restrict__ dz,
+    float* __restrict__ sums, int pieces) {
+  constexpr bool GLU = ACT == LRMOE_ACT_SWIGLU;
+  constexpr int H = GLU ? 2 : 1;
+  __shared__ float part[kWaves - 1][H * N][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t run = blockIdx.x / pieces;
+  const int col = (int)(blockIdx.x % pieces) * (64 * N) + lane * N;
+  int e;
+  int64_t sub;
+  if (!find_run(seg, E, P, run, e, sub)) return;   // the same answer in every wave
+  int64_t lo, hi;
+  segment(seg, e, P, lo, hi);
+  lo += sub * kRows;
+  if (hi > lo + kRows) hi = lo + kRows;
+  float acc[H][N];
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[h][i] = 0.f;
+  if (col < F)
+#pragma unroll 2
+    for (int64_t u = lo + wave; u < hi; u += kWaves) {
+      float g[N], a[N], b[N];
+      load_vals(dy + u * F + col, g);
+      if (ACT != LRMOE_ACT_NONE) load_vals(pa + u * F + col, a);
+      if (GLU) load_vals(pb + u * F + col, b);
+      float z[H][N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if constexpr (GLU) {
+          const float s = sigmoid_f32(a[i]);
+          z[0][i] = g[i] * b[i] * (s * (1.f + a[i] * (1.f - s)));
+          z[H - 1][i] = g[i] * (a[i] * s);
+        } else if constexpr (ACT == LRMOE_ACT_RELU) {
+          z[0][i] = a[i] > 0.f ? g[i] : 0.f;
+        } else if constexpr (ACT == LRMOE_ACT_NONE) {
+          z[0][i] = g[i];
+        } else {
+          z[0][i] = g[i] * act_grad<ACT>(a[i]);
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        store_vals(dz + (u * H + h) * F + col, z[h]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[h][i] += z[h][i];
+      }
+    }
+  if (sums == nullptr) return;
+  if (wave > 0)
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int i = 0; i < N; ++i) part[wave - 1][h * N + i][lane] = acc[h][i];
+  __syncthreads();
+  if (wave == 0 && col < F) {
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int w = 0; w < kWaves - 1; ++w) acc[h][i] += part[w][h * N + i][lane];
+      store_vals(sums + (run * H + h) * F + col, acc[h]);
+    }
+  }
+}
+
+// dbias[e] = the expert's runs, added in order; 0 for an expert without rows.
+__global__ __launch_bounds__(kThreads) void dbias_kernel(const int32_t* __restrict__ seg,
+                                                         int64_t P, int width, int64_t limit,
+                                                         const float* __restrict__ sums,
+                                                         float* __restrict__ dbias) {
+  const int e = blockIdx.y, col = blockIdx.x * kThreads + threadIdx.x;
+  const int lane = threadIdx.x & 63;
+  int64_t first = 0, lo, hi;
+  for (int i = lane; i < e; i += 64) {
+    segment(seg, i, P, lo, hi);
+    first += runs_of(hi - lo);
+  }
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) first += __shfl_xor(first, m, 64);
+  if (col >= width) return;
+  segment(seg, e, P, lo, hi);
+  // offsets that do not ascend may name more runs than there are: never read past them
+  int64_t end = first + runs_of(hi - lo);
+  if (end > limit) end = limit;
+  float s = 0.f;
+#pragma unroll 8
+  for (int64_t r = first; r < end; ++r) s += sums[r * width + col];
+  dbias[(int64_t)e * width + col] = s;
+}
+
+template <typename T, typename TO, int N>
+hipError_t run(int act, const int32_t* seg, const void* dy, const void* a, const void* b, int64_t P,
+               int E, int F, void* dz, float* sums, hipStream_t s) {
+  const int pieces = (F + 64 * N - 1) / (64 * N);
+  const int64_t blocks = max_runs(P, E) * pieces;
+  if (blocks == 0) return hipSuccess;
+  if (blocks >= int64_t(1) << 24) return hipErrorInvalidValue;   // 2^32 threads
+  const dim3 grid((uint32_t)blocks), block(kThreads);
+#define LRMOE_ACT(A)                                                                            \
+  case A:                                                                                       \
+    hipLaunchKernelGGL((act_backward_kernel<T, TO, N, A>), grid, block, 0, s, seg,              \
+                       static_cast<const T*>(dy), static_cast<const T*>(a),                     \
+                       static_cast<const T*>(b), P, E, F, static_cast<TO*>(dz), sums, pieces);  \
+    break
+  switch (act) {
+    LRMOE_ACT(LRMOE_ACT_NONE);
+    LRMOE_ACT(LRMOE_ACT_RELU);
+    LRMOE_ACT(LRMOE_ACT_SILU);
+    LRMOE_ACT(LRMOE_ACT_GELU);
+    LRMOE_ACT(LRMOE_ACT_SWIGLU);
+  }
+#undef LRMOE_ACT
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t act_backward_workspace(int64_t P, int32_t E, int32_t width, bool dbias) {
+  return dbias ? (size_t)max_runs(P, E) * width * sizeof(float) : 0;
+}
+
+hipError_t launch_act_backward(int dtype, int out_dtype, int act, const int32_t* seg,
+                               const void* dy, const void* a, const void* b, int64_t P, int32_t E,
+                               int32_t F, void* dz, float* dbias, float* ws, hipStream_t s) {
+  float* sums = dbias != nullptr ? ws : nullptr;
+  hipError_t err;
+  if (dtype == LRMOE_BF16 && out_dtype == LRMOE_BF16)
+    err = run<uint16_t, uint16_t, 8>(act, seg, dy, a, b, P, E, F, dz, sums, s);
+  else if (dtype == LRMOE_BF16)
+    err = run<uint16_t, float, 8>(act, seg, dy, a, b, P, E, F, dz, sums, s);
+  else
+    err = run<float, float, 4>(act, seg, dy, a, b, P, E, F, dz, sums, s);
+  if (err != hipSuccess || dbias == nullptr) return err;
+  const int width = F * (act == LRMOE_ACT_SWIGLU ? 2 : 1);
+  hipLaunchKernelGGL(dbias_kernel, dim3((width + kThreads - 1) / kThreads, E), dim3(kThreads), 0, s,
+                     seg, P, width, max_runs(P, E), sums, dbias);
+  return hipGetLastError();
+}
+
+}  // namespace lrmoe

@@ -20,7 +20,11 @@ F32, BF16 = 0, 1
 DW_EXACT, DW_BF16, DW_F16 = 0, 1, 2
 SCORE_LRM, SCORE_GRAD_SQNORM, SCORE_GRAD_L1 = 0, 1, 2
 QUOTA_RATIO, QUOTA_BUDGET = 0, 1
+GATE_SOFTMAX, GATE_SIGMOID = 0, 1
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_SWIGLU = 0, 1, 2, 3, 4
 MAX_EXPERTS = 256
+MAX_GATE_EXPERTS = 1024
+MAX_TOPK = 64
 ABI_VERSION = 4
 
 STATUS = {0: "LRMOE_OK", 1: "LRMOE_ERR_NULL", 2: "LRMOE_ERR_INVALID", 3: "LRMOE_ERR_SHAPE",
@@ -35,7 +39,11 @@ EXPORTS = ["lrmoe_abi_version", "lrmoe_status_string", "lrmoe_plan_quota",
            "lrmoe_grouped_backward_glu_timed", "lrmoe_pruned_backward",
            "lrmoe_pruned_backward_timed", "lrmoe_gather_backward",
            "lrmoe_gather_backward_timed", "lrmoe_grouped_backward_gate_up",
-           "lrmoe_grouped_backward_gate_up_timed", "lrmoe_score_select_compact_noalloc"]
+           "lrmoe_grouped_backward_gate_up_timed", "lrmoe_score_select_compact_noalloc",
+           "lrmoe_gate_topk", "lrmoe_gate_topk_backward", "lrmoe_route_sort_workspace",
+           "lrmoe_route_sort", "lrmoe_dispatch", "lrmoe_dispatch_backward", "lrmoe_combine",
+           "lrmoe_combine_backward", "lrmoe_grouped_forward", "lrmoe_act_backward_workspace",
+           "lrmoe_act_backward"]
 TIMING_SLOTS = 8
 
 
@@ -59,6 +67,16 @@ class Timing(C.Structure):
 class QuotaPolicy(C.Structure):
     _fields_ = [("mode", C.c_int32), ("num", C.c_int64), ("den", C.c_int64),
                 ("budget_pairs", C.c_int64)]
+
+
+class Gate(C.Structure):
+    _fields_ = [("T", C.c_int64), ("E", C.c_int32), ("K", C.c_int32), ("dtype", C.c_int32),
+                ("score", C.c_int32), ("renorm", C.c_int32), ("scale", C.c_float)]
+
+
+class Forward(C.Structure):
+    _fields_ = [("E", C.c_int32), ("dtype", C.c_int32), ("P", C.c_int64), ("T", C.c_int64),
+                ("d_out", C.c_int32), ("d_in", C.c_int32), ("act", C.c_int32)]
 
 
 _lib_handle = None
@@ -128,6 +146,21 @@ def lib() -> C.CDLL:
                                                        [C.c_size_t, _P, C.POINTER(Timing)])
     L.lrmoe_score_select_compact_noalloc.restype = C.c_int
     L.lrmoe_score_select_compact_noalloc.argtypes = [C.POINTER(Problem)] + [_P] * 13
+    i32, i64 = C.c_int32, C.c_int64
+    for name, args in (
+            ("lrmoe_gate_topk", [C.POINTER(Gate)] + [_P] * 5),
+            ("lrmoe_gate_topk_backward", [C.POINTER(Gate)] + [_P] * 5),
+            ("lrmoe_route_sort_workspace", [i64, i32, i32, C.POINTER(C.c_size_t)]),
+            ("lrmoe_route_sort", [i64, i32, i32] + [_P] * 8 + [C.c_size_t, _P]),
+            ("lrmoe_dispatch", [i32, i64, i32, i32, i64] + [_P] * 4),
+            ("lrmoe_dispatch_backward", [i32, i32, i64, i32, i32, i64] + [_P] * 4),
+            ("lrmoe_combine", [i32, i64, i32, i32, i64] + [_P] * 6),
+            ("lrmoe_combine_backward", [i32, i64, i32, i32, i64] + [_P] * 7),
+            ("lrmoe_grouped_forward", [C.POINTER(Forward)] + [_P] * 10),
+            ("lrmoe_act_backward_workspace", [C.POINTER(Forward), C.POINTER(C.c_size_t)]),
+            ("lrmoe_act_backward", [C.POINTER(Forward), i32] + [_P] * 7 + [C.c_size_t, _P])):
+        fn = getattr(L, name)
+        fn.restype, fn.argtypes = C.c_int, args
     if L.lrmoe_abi_version() != ABI_VERSION:
         raise RuntimeError("liblrmoe ABI version mismatch; rebuild the library")
     _lib_handle = L
@@ -602,4 +635,272 @@ def pruned_backward(plan: Plan, alpha, g, phi, W, g_row_index=None, out=None, ws
               lib().lrmoe_pruned_backward_timed(*args, C.byref(timing.next_slots())))
     else:
         check("lrmoe_pruned_backward", lib().lrmoe_pruned_backward(*args))
+    return out
+
+
+# --------------------------------------------------------------- forward side
+# Router gate, expert sort, dispatch, grouped product and combine, with their
+# gradients.  Tensors may live on any one GPU; the calls go to that GPU's
+# current stream.
+
+def _arg(name: str, t: torch.Tensor, dtype, shape, dev):
+    """Device address of an argument, after checking it."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {dtype} expected, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {shape} expected, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, the other tensors are on {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: liblrmoe takes contiguous tensors")
+    return t.data_ptr() if t.numel() > 0 else None
+
+
+def _device(t: torch.Tensor):
+    if not t.is_cuda:
+        raise ValueError("liblrmoe takes device tensors")
+    return t.device
+
+
+def _call(fn: str, dev, *args) -> None:
+    """Run an entry point on `dev` (its last argument, the stream, is added)."""
+    f = getattr(lib(), fn)
+    if dev.index == torch.cuda.current_device():
+        st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    check(fn, st)
+
+
+def _workspace(need: int, ws: Optional[torch.Tensor], dev):
+    """(address, bytes) of a caller's workspace, or of one made for this call.
+    The library checks the size."""
+    if ws is None:
+        ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+    elif ws.device != dev:
+        raise ValueError(f"workspace: on {ws.device}, the other tensors are on {dev}")
+    elif not ws.is_contiguous():
+        raise ValueError("workspace: liblrmoe takes contiguous tensors")
+    if ws is None:
+        return None, 0, None
+    n = ws.numel() * ws.element_size()
+    return (ws.data_ptr() if n else None), n, ws
+
+
+def _rank(name: str, t: torch.Tensor, n: int):
+    if t.dim() != n:
+        raise ValueError(f"{name}: {n} dimensions expected, got {t.dim()}")
+
+
+def gate_topk(logits, k: int, score: int = GATE_SOFTMAX, select_bias=None, renorm: bool = True,
+              scale: float = 1.0, out: Optional[dict] = None) -> dict:
+    """Top-k router gate: ids int32 [T, k] (best first, ties to the lower
+    expert, -1 where nothing is left to choose) and weights float32 [T, k]
+    from logits [T, E].  select_bias (float32 [E], sigmoid score) enters the
+    selection only."""
+    dev = _device(logits)
+    _rank("logits", logits, 2)
+    T, E = logits.shape
+    g = Gate(T, E, int(k), storage_dtype(logits.dtype), int(score), int(bool(renorm)), float(scale))
+    if out is None:
+        n = max(int(k), 0)
+        out = dict(ids=_empty((T, n), torch.int32, dev), weights=_empty((T, n), torch.float32, dev))
+    _call("lrmoe_gate_topk", dev, C.byref(g), _arg("logits", logits, logits.dtype, (T, E), dev),
+          None if select_bias is None else _arg("select_bias", select_bias, torch.float32, (E,), dev),
+          _arg("ids", out["ids"], torch.int32, (T, int(k)), dev),
+          _arg("weights", out["weights"], torch.float32, (T, int(k)), dev))
+    return out
+
+
+def gate_topk_backward(logits, ids, dweights, score: int = GATE_SOFTMAX, renorm: bool = True,
+                       scale: float = 1.0, dlogits=None) -> torch.Tensor:
+    """dlogits [T, E] (the logits' type) from dweights [T, k] at ids [T, k]."""
+    dev = _device(logits)
+    _rank("logits", logits, 2)
+    _rank("ids", ids, 2)
+    T, E = logits.shape
+    k = ids.shape[1]
+    g = Gate(T, E, k, storage_dtype(logits.dtype), int(score), int(bool(renorm)), float(scale))
+    if dlogits is None:
+        dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
+    _call("lrmoe_gate_topk_backward", dev, C.byref(g),
+          _arg("logits", logits, logits.dtype, (T, E), dev),
+          _arg("ids", ids, torch.int32, (T, k), dev),
+          _arg("dweights", dweights, torch.float32, (T, k), dev),
+          _arg("dlogits", dlogits, logits.dtype, (T, E), dev))
+    return dlogits
+
+
+def route_sort_workspace_bytes(T: int, K: int, E: int) -> int:
+    n = C.c_size_t(0)
+    check("lrmoe_route_sort_workspace", lib().lrmoe_route_sort_workspace(T, K, E, C.byref(n)))
+    return int(n.value)
+
+
+def route_sort(ids, E: int, weights=None, out: Optional[dict] = None, ws=None) -> dict:
+    """Stable sort of the slots of ids [T, K] by expert: counts int64 [E],
+    seg_offsets int32 [E + 1], row_index int32 [T * K] (token of each pair),
+    pos int32 [T, K] (place of each slot, -1 for ids outside 0..E-1) and, with
+    weights [T, K], alpha float32 [T * K]."""
+    dev = _device(ids)
+    _rank("ids", ids, 2)
+    T, K = ids.shape
+    need = route_sort_workspace_bytes(T, K, int(E))
+    if out is None:
+        out = dict(counts=_empty((E,), torch.int64, dev),
+                   seg_offsets=_empty((E + 1,), torch.int32, dev),
+                   row_index=_empty((T * K,), torch.int32, dev),
+                   pos=_empty((T, K), torch.int32, dev))
+        if weights is not None:
+            out["alpha"] = _empty((T * K,), torch.float32, dev)
+    addr, n, _keep = _workspace(need, ws, dev)
+    alpha = out.get("alpha")
+    _call("lrmoe_route_sort", dev, T, K, int(E), _arg("ids", ids, torch.int32, (T, K), dev),
+          None if weights is None else _arg("weights", weights, torch.float32, (T, K), dev),
+          _arg("counts", out["counts"], torch.int64, (E,), dev),
+          _arg("seg_offsets", out["seg_offsets"], torch.int32, (E + 1,), dev),
+          _arg("row_index", out["row_index"], torch.int32, (T * K,), dev),
+          _arg("pos", out["pos"], torch.int32, (T, K), dev),
+          None if alpha is None else _arg("alpha", alpha, torch.float32, (T * K,), dev),
+          addr, n)
+    return out
+
+
+def dispatch(x, pos, xp=None) -> torch.Tensor:
+    """xp[pos[t, k]] = x[t]; xp has one row per slot unless it is given (rows
+    that no slot names are left as they were)."""
+    dev = _device(x)
+    _rank("x", x, 2)
+    _rank("pos", pos, 2)
+    T, D = x.shape
+    K = pos.shape[1]
+    if xp is None:
+        xp = _empty((T * K, D), x.dtype, dev)
+    P = xp.shape[0]
+    _call("lrmoe_dispatch", dev, storage_dtype(x.dtype), T, K, D, P,
+          _arg("x", x, x.dtype, (T, D), dev), _arg("pos", pos, torch.int32, (T, K), dev),
+          _arg("xp", xp, x.dtype, (P, D), dev))
+    return xp
+
+
+def dispatch_backward(dxp, pos, dtype: Optional[torch.dtype] = None, dx=None) -> torch.Tensor:
+    """dx[t] = sum_k dxp[pos[t, k]] in `dtype` (default: dxp's)."""
+    dev = _device(dxp)
+    _rank("dxp", dxp, 2)
+    _rank("pos", pos, 2)
+    P, D = dxp.shape
+    T, K = pos.shape
+    if dx is None:
+        dx = _empty((T, D), dtype or dxp.dtype, dev)
+    elif dtype is not None and dx.dtype != dtype:
+        raise TypeError(f"dx: {dtype} expected, got {dx.dtype}")
+    _call("lrmoe_dispatch_backward", dev, storage_dtype(dxp.dtype), storage_dtype(dx.dtype), T, K, D,
+          P, _arg("dxp", dxp, dxp.dtype, (P, D), dev), _arg("pos", pos, torch.int32, (T, K), dev),
+          _arg("dx", dx, dx.dtype, (T, D), dev))
+    return dx
+
+
+def combine(yp, pos, weights, residual=None, y=None) -> torch.Tensor:
+    """y[t] = residual[t] + sum_k weights[t, k] * yp[pos[t, k]]."""
+    dev = _device(yp)
+    _rank("yp", yp, 2)
+    _rank("pos", pos, 2)
+    P, D = yp.shape
+    T, K = pos.shape
+    if y is None:
+        y = _empty((T, D), yp.dtype, dev)
+    _call("lrmoe_combine", dev, storage_dtype(yp.dtype), T, K, D, P,
+          _arg("yp", yp, yp.dtype, (P, D), dev), _arg("pos", pos, torch.int32, (T, K), dev),
+          _arg("weights", weights, torch.float32, (T, K), dev),
+          None if residual is None else _arg("residual", residual, yp.dtype, (T, D), dev),
+          _arg("y", y, yp.dtype, (T, D), dev))
+    return y
+
+
+def combine_backward(dy, yp, pos, weights, out: Optional[dict] = None) -> dict:
+    """Gradient of combine: dyp [P, D] (rows that no slot names are left as
+    they were) and dweights float32 [T, K]."""
+    dev = _device(dy)
+    _rank("yp", yp, 2)
+    _rank("pos", pos, 2)
+    P, D = yp.shape
+    T, K = pos.shape
+    if out is None:
+        out = dict(dyp=_empty((P, D), yp.dtype, dev), dweights=_empty((T, K), torch.float32, dev))
+    _call("lrmoe_combine_backward", dev, storage_dtype(yp.dtype), T, K, D, P,
+          _arg("dy", dy, yp.dtype, (T, D), dev), _arg("yp", yp, yp.dtype, (P, D), dev),
+          _arg("pos", pos, torch.int32, (T, K), dev),
+          _arg("weights", weights, torch.float32, (T, K), dev),
+          _arg("dyp", out["dyp"], yp.dtype, (P, D), dev),
+          _arg("dweights", out["dweights"], torch.float32, (T, K), dev))
+    return out
+
+
+def grouped_forward(seg_offsets, x, W, row_index=None, bias=None, residual=None,
+                    act: int = ACT_NONE, save_pre: bool = False, out: Optional[dict] = None) -> dict:
+    """y_u = act(W_e x_row(u) + bias_e) + residual_u for the pairs of each
+    segment of seg_offsets (device int32 [E + 1]).  x [T, d_in] is read through
+    row_index [P] (None: row u of pair u), W is [E, d_out, d_in].  Returns y
+    [P, F] (F = d_out, or d_out / 2 for ACT_SWIGLU) and, with save_pre, the
+    pre-activations pre_a (and pre_b).  Rows behind the last segment are left
+    as they were."""
+    dev = _device(x)
+    _rank("x", x, 2)
+    _rank("W", W, 3)
+    T, d_in = x.shape
+    E, d_out, dt = W.shape[0], W.shape[1], x.dtype
+    P = T if row_index is None else row_index.numel()
+    glu = act == ACT_SWIGLU
+    F = d_out // 2 if glu else d_out
+    if out is None:
+        out = dict(y=_empty((P, F), dt, dev))
+        if save_pre:
+            out["pre_a"] = _empty((P, F), dt, dev)
+            if glu:
+                out["pre_b"] = _empty((P, F), dt, dev)
+    fw = Forward(E, storage_dtype(dt), P, T, d_out, d_in, int(act))
+    pa, pb = out.get("pre_a"), out.get("pre_b")
+    _call("lrmoe_grouped_forward", dev, C.byref(fw),
+          _arg("seg_offsets", seg_offsets, torch.int32, (E + 1,), dev),
+          None if row_index is None else _arg("row_index", row_index, torch.int32, (P,), dev),
+          _arg("x", x, dt, (T, d_in), dev), _arg("W", W, dt, (E, d_out, d_in), dev),
+          None if bias is None else _arg("bias", bias, dt, (E, d_out), dev),
+          None if residual is None else _arg("residual", residual, dt, (P, F), dev),
+          _arg("y", out["y"], dt, (P, F), dev),
+          None if pa is None else _arg("pre_a", pa, dt, (P, F), dev),
+          None if pb is None else _arg("pre_b", pb, dt, (P, F), dev))
+    return out
+
+
+def act_backward(seg_offsets, dy, pre_a=None, pre_b=None, act: int = ACT_NONE, dbias: bool = True,
+                 dz_dtype: Optional[torch.dtype] = None, out: Optional[dict] = None,
+                 ws=None) -> dict:
+    """Gradient of grouped_forward's epilogue: dz [P, d_out] (gate half first
+    for ACT_SWIGLU; type dz_dtype, default dy's) and dbias float32 [E, d_out]
+    (None without).  dz then goes through grouped_backward with quotas =
+    counts, or as float32 through grouped_backward_gate_up."""
+    dev = _device(dy)
+    _rank("dy", dy, 2)
+    P, F = dy.shape
+    E, dt = seg_offsets.numel() - 1, dy.dtype
+    d_out = 2 * F if act == ACT_SWIGLU else F
+    if out is None:
+        out = dict(dz=_empty((P, d_out), dz_dtype or dt, dev),
+                   dbias=_empty((E, d_out), torch.float32, dev) if dbias else None)
+    dz, db = out["dz"], out.get("dbias")
+    # d_in plays no part here; any row length the library takes
+    fw = Forward(E, storage_dtype(dt), P, P, d_out, 8, int(act))
+    need = C.c_size_t(0)
+    if db is not None:
+        check("lrmoe_act_backward_workspace",
+              lib().lrmoe_act_backward_workspace(C.byref(fw), C.byref(need)))
+    addr, n, _keep = _workspace(int(need.value), ws, dev)
+    _call("lrmoe_act_backward", dev, C.byref(fw), storage_dtype(dz.dtype),
+          _arg("seg_offsets", seg_offsets, torch.int32, (E + 1,), dev),
+          _arg("dy", dy, dt, (P, F), dev),
+          None if pre_a is None else _arg("pre_a", pre_a, dt, (P, F), dev),
+          None if pre_b is None else _arg("pre_b", pre_b, dt, (P, F), dev),
+          _arg("dz", dz, dz.dtype, (P, d_out), dev),
+          None if db is None else _arg("dbias", db, torch.float32, (E, d_out), dev), addr, n)
     return out
