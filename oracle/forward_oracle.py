@@ -170,14 +170,18 @@ def linear(seg, x, W, row_index=None, bias=None, residual=None, name="none"):
     z = torch.zeros((P, d_out), dtype=torch.float64)
     mag = torch.zeros((P, d_out), dtype=torch.float64)
     for e in range(E):
-        for u in range(int(seg[e]), int(seg[e + 1])):
-            r = u if row_index is None else int(row_index[u])
-            v = x[r].double() if 0 <= r < x.shape[0] else torch.zeros(d_in, dtype=torch.float64)
-            z[u] = W[e].double() @ v
-            mag[u] = W[e].double().abs() @ v.abs()
-            if bias is not None:
-                z[u] += bias[e].double()
-                mag[u] += bias[e].double().abs()
+        rows = [u if row_index is None else int(row_index[u])
+                for u in range(int(seg[e]), int(seg[e + 1]))]
+        if not rows:
+            continue
+        v = torch.stack([x[r].double() if 0 <= r < x.shape[0]
+                         else torch.zeros(d_in, dtype=torch.float64) for r in rows])
+        at = slice(int(seg[e]), int(seg[e + 1]))
+        z[at] = v @ W[e].double().t()
+        mag[at] = v.abs() @ W[e].double().abs().t()
+        if bias is not None:
+            z[at] += bias[e].double()
+            mag[at] += bias[e].double().abs()
     if name == "swiglu":
         F = d_out // 2
         y = act(name, z[:, :F], z[:, F:])

@@ -12,6 +12,10 @@
 // (v_mfma_f32_32x32x16_bf16, 8 values a fragment) and float32
 // (v_mfma_f32_32x32x2_f32, 4 values a fragment, four products), float32
 // accumulation in both.  Masked rows and the end of K read a page of zeros.
+#include <algorithm>
+#include <type_traits>
+#include <utility>
+
 #include "forward.h"
 
 namespace lrmoe {
@@ -35,6 +39,10 @@ __device__ __forceinline__ float activate(int act, float x) {
 }
 
 // ---------------------------------------------------------------- tiles
+// Row tiles that take their turns at each column tile together, and so share
+// its panel of W in the L2.
+constexpr int kGroup = 8;
+
 struct TileAt {
   int e;
   int64_t lo;    // first pair row of the tile
@@ -43,11 +51,11 @@ struct TileAt {
 };
 
 // Tile of this workgroup, or false.  Workgroup b runs on XCD b % 8, so each
-// XCD takes a contiguous eighth of the tiles; inside it, group rows tiles
-// share their W panels, column by column.  Each wave finds the tile for
+// XCD takes a contiguous eighth of the tiles; inside it, kGroup row tiles go
+// column by column.  Each wave finds the tile for
 // itself: lane l counts the tiles of experts 4 l .. 4 l + 3.
 __device__ __forceinline__ bool find_tile(const int32_t* seg, int E, int64_t P, int tm, int cols,
-                                          int group, TileAt& at) {
+                                          TileAt& at) {
   const int lane = threadIdx.x & 63;
   int64_t off[5];
 #pragma unroll
@@ -73,12 +81,12 @@ __device__ __forceinline__ bool find_tile(const int32_t* seg, int E, int64_t P, 
   const int64_t share = (total + 7) / 8;
   const int64_t t = (int64_t)(blockIdx.x & 7) * share + (blockIdx.x >> 3);
   if ((int64_t)(blockIdx.x >> 3) >= share || t >= total) return false;
-  const int64_t per = (int64_t)group * cols;
+  const int64_t per = (int64_t)kGroup * cols;
   const int g = (int)(t / per);
   const int in = (int)(t - g * per);
-  const int left = all - g * group;
-  const int gr = left < group ? left : group;
-  const int r = __builtin_amdgcn_readfirstlane(g * group + in % gr);
+  const int left = all - g * kGroup;
+  const int gr = left < kGroup ? left : kGroup;
+  const int r = __builtin_amdgcn_readfirstlane(g * kGroup + in % gr);
   at.col = __builtin_amdgcn_readfirstlane(in / gr);
   const int owner = __ffsll((unsigned long long)__ballot(end > r)) - 1;
   int sub = r - (end - sum), j = 0;   // meant for the owner lane
@@ -107,30 +115,24 @@ __device__ __forceinline__ const char* x_row(const ForwardArgs& a, int64_t u) {
   return reinterpret_cast<const char*>(static_cast<const T*>(a.x) + r * a.d_in);
 }
 
-// 16-byte value of one lane times one lane's: four float32 products or one bf16.
-template <typename T>
-__device__ __forceinline__ f32x16 mfma32(vec4u a, vec4u b, f32x16 c) {
+// Products of 16-byte fragments (MI x MI results): one bf16 product of 16
+// (MI = 32) or 32 (MI = 16) values of K, or four float32 products of 2 or 4
+// values.
+template <int MI>
+using Acc = typename std::conditional<MI == 32, f32x16, f32x4>::type;
+template <typename T, int MI>
+__device__ __forceinline__ Acc<MI> mfma(vec4u a, vec4u b, Acc<MI> c) {
   if constexpr (sizeof(T) == 2) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    const bf16x8 x = __builtin_bit_cast(bf16x8, a), y = __builtin_bit_cast(bf16x8, b);
+    if constexpr (MI == 32) return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, c, 0, 0, 0);
+    else return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c, 0,
-                                               0, 0);
-    return c;
-  }
-}
-template <typename T>
-__device__ __forceinline__ f32x4 mfma16(vec4u a, vec4u b, f32x4 c) {
-  if constexpr (sizeof(T) == 2) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c, 0,
-                                               0, 0);
+    for (int i = 0; i < 4; ++i) {
+      const float x = __uint_as_float(a[i]), y = __uint_as_float(b[i]);
+      if constexpr (MI == 32) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x, y, c, 0, 0, 0);
+      else c = __builtin_amdgcn_mfma_f32_16x16x4f32(x, y, c, 0, 0, 0);
+    }
     return c;
   }
 }
@@ -138,7 +140,21 @@ __device__ __forceinline__ f32x4 mfma16(vec4u a, vec4u b, f32x4 c) {
 // ---- global -> LDS, 16 bytes a lane: lane i writes LDS bytes [lds + 16 i,
 // lds + 16 i + 16).  Inline asm without outputs: the compiler then does not
 // wait for it before LDS reads of other stages; the explicit waits below
-// order the stages.
+// order the stages.  The buffer form reads zeros past its range.
+constexpr uint32_t kBufferFlags = 0x00020000u;   // gfx9 family: raw 32-bit data
+constexpr uint32_t kOutOfRange = 0x80000000u;    // offset that is never in range
+constexpr int64_t kNearBytes = int64_t(1) << 31; // what one buffer reaches
+// Each column tile of each expert starts its K loop this many K steps after
+// its neighbour's and goes round: rows of W a power of two apart would else
+// have all workgroups on the same few memory channels at a time (4096 columns:
+// 87 us against 68 us for 369 MB of W; other strides are unchanged).
+constexpr int kStagger = 3;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0,
+                                           (int)(bytes > 0x7FFFFFFF ? 0x7FFFFFFF : bytes),
+                                           (int)kBufferFlags);
+}
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_lds16(uint32_t lds, const char* p) {
@@ -146,34 +162,53 @@ __device__ __forceinline__ void load_lds16(uint32_t lds, const char* p) {
                "v"(p)
                : "memory", "m0");
 }
+__device__ __forceinline__ void load_lds16(uint32_t lds, __amdgpu_buffer_rsrc_t r, uint32_t voff,
+                                           uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds),
+               "v"(voff), "s"(r), "s"(soff)
+               : "memory", "m0");
+}
 #pragma clang diagnostic pop
+
+// f(0), f(1), ... f(N - 1), each with its index as a compile-time constant.
+template <typename F, int... I>
+__device__ __forceinline__ void static_for_(F& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_(f, std::make_integer_sequence<int, N>());
+}
 
 template <int N>
 __device__ __forceinline__ void wait_loads_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// T: storage.  MB x NB 32x32 blocks a wave, WM x WN waves.  RB: bytes of one
-// row in one K step (64 or 128).  NS: LDS stages.
-template <typename T, int MB, int NB, int WM, int WN, int RB, int NS, bool GLU>
+// T: storage.  MI: size of an MFMA result.  A wave computes WR x WC, WM x WN
+// waves a workgroup.  RB: bytes of one row in one K step (64 or 128).  NS:
+// LDS stages.
+template <typename T, int MI, int WR, int WC, int WM, int WN, int RB, int NS, bool GLU,
+          bool FAR = false>
 struct Gemm {
+  static constexpr int kMI = MI, MB = WR / MI, NB = WC / MI;
   static constexpr int kMB = MB, kNB = NB;
   static constexpr int kWaves = WM * WN;
-  static constexpr int kWavesPerSimd = MB * NB > 8 ? 1 : 2;
   static constexpr int kThreads = 64 * kWaves;
-  static constexpr int TM = WM * MB * 32, TN = WN * NB * 32;
+  static constexpr int kWavesPerSimd = WR * WC > 8192 ? 1 : 2;
+  static constexpr int TM = WM * WR, TN = WN * WC;
   static constexpr int kOut = GLU ? TN / 2 : TN;           // columns of y
-  static constexpr int kSlices = RB / 32;                  // MFMA steps of a K step
+  static constexpr int kSliceBytes = MI == 32 ? 32 : 64;   // K bytes of one MFMA
+  static constexpr int kSlices = RB / kSliceBytes;         // MFMA steps of a K step
+  static constexpr int kUnroll = kSlices % 2 ? 2 : 1;      // K steps a round: fragment sets alternate
   static constexpr int kChunks = RB / 16;
   static constexpr int kStage = (TM + TN) * RB;
   static constexpr int kPwA = TM * RB / 1024 / kWaves, kPwB = TN * RB / 1024 / kWaves;
   static constexpr int kLoads = kPwA + kPwB;               // load instructions a stage and wave
-  static constexpr int kEpi = kWaves * NB * 4096;          // epilogue staging
-  static constexpr int kMain = NS * kStage > kEpi ? NS * kStage : kEpi;
-  static constexpr int kLds = kMain + kWaves * 1024;       // + a sink for loads past the end
+  static constexpr int kEpi = kWaves * WC * 128;           // epilogue staging
+  static constexpr int kLds = NS * kStage > kEpi ? NS * kStage : kEpi;
   static_assert(TM * RB % (1024 * kWaves) == 0 && TN * RB % (1024 * kWaves) == 0, "whole loads");
   static_assert(!GLU || NB % 2 == 0, "gate and up blocks of a wave");
-  static_assert(kSlices % 2 == 0, "fragment sets alternate");
 
   // Chunk c of row r sits at slot c ^ swz(r): 16 consecutive rows of one chunk
   // (one LDS cycle of a 16-byte read) fall on 16 distinct bank groups.
@@ -181,17 +216,18 @@ struct Gemm {
     return RB == 64 ? (r ^ (r >> 2)) & 3 : (r >> 1) & 7;
   }
 
-  struct Frags {
-    vec4u a[MB], b[NB];
-  };
-
   const ForwardArgs& args;
   uint32_t lds;            // LDS byte address of stage 0
   int lane, wave, wm, wn;
-  int kbytes, nk;
-  const char* src[kLoads]; // this lane's next 16 bytes of each load
-  int step[kLoads];        // bytes to the next K step (0 for masked rows)
-  int chunk[kLoads];       // byte offset of the lane's chunk inside the step
+  int kbytes, nk, k0;
+  // Where this lane reads each of its loads.  Near: byte offsets into the
+  // buffers of x and of the expert's weights, fixed over K.  Far (x or one
+  // expert's weights beyond 2 GiB): addresses, advanced with K.
+  __amdgpu_buffer_rsrc_t xbuf, wbuf;
+  uint32_t off[FAR ? 1 : kLoads];
+  const char* src[FAR ? kLoads : 1];
+  int step[FAR ? kLoads : 1];
+  int chunk[2];            // byte offset of the lane's chunk inside the step, by block parity
   uint32_t fa, fb;         // fragment base addresses (A rows, B rows of the wave)
   uint32_t fs[kSlices];    // lane's offset of each slice
 
@@ -204,117 +240,165 @@ struct Gemm {
     wn = wave % WN;
     kbytes = a.d_in * (int)sizeof(T);
     nk = (kbytes + RB - 1) / RB;
-    const char* zero = reinterpret_cast<const char*>(zero_page);
+    k0 = 0;
+    if constexpr (!FAR) k0 = (at.e * 64 + at.col) * kStagger % (nk < 64 ? nk : 64);
     const int F = GLU ? a.d_out / 2 : a.d_out;
+    const char* W = static_cast<const char*>(a.W) + (int64_t)at.e * a.d_out * kbytes;
+    const char* x = static_cast<const char*>(a.x);
+    if (!FAR) {
+      int64_t rows = a.T;
+      if (a.row_index == nullptr) {   // the tile's own rows
+        x += at.lo * kbytes;
+        rows = at.rows;
+      }
+      xbuf = buffer(x, rows * kbytes);
+      wbuf = buffer(W, (int64_t)a.d_out * kbytes);
+    }
     constexpr int rows_per = 1024 / RB;
+    static_assert(kPwA % 2 == 0 || kWaves % 2 == 0 || RB == 64, "block parity");
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      chunk[j] = ((lane % kChunks) ^ swz(j * rows_per + lane / kChunks)) * 16;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
       const bool isA = j < kPwA;
       const int blk = isA ? wave * kPwA + j : wave * kPwB + j - kPwA;
       const int r = blk * rows_per + lane / kChunks;
-      chunk[j] = ((lane % kChunks) ^ swz(r)) * 16;
-      const char* p = nullptr;
+      const int ch = ((lane % kChunks) ^ swz(r)) * 16;
+      int64_t n;   // row of x or of the expert's weights
+      bool ok;
       if (isA) {
-        if (r < at.rows) p = x_row<T>(a, at.lo + r);
+        ok = r < at.rows;
+        n = ok && a.row_index != nullptr ? (int64_t)a.row_index[at.lo + r]
+                                         : (FAR ? at.lo + r : (int64_t)r);
+        ok = ok && n >= 0 && n < (a.row_index != nullptr || FAR ? a.T : (int64_t)at.rows);
+      } else if constexpr (GLU) {
+        // LDS row r holds, of wave column w = r / WC, first the gate rows and
+        // then the up rows of the wave's output columns
+        constexpr int half = WC / 2;
+        const int w = r / WC, i = r % WC;
+        const int c = at.col * kOut + w * half + i % half;
+        ok = c < F;
+        n = (int64_t)(i / half) * F + c;
       } else {
-        // LDS row r holds, for SwiGLU, of wave column w = r / (NB * 32) first
-        // the gate rows and then the up rows of the wave's output columns
-        int64_t n;
-        bool ok;
-        if constexpr (GLU) {
-          constexpr int half = NB * 16;
-          const int w = r / (NB * 32), i = r % (NB * 32);
-          const int c = at.col * kOut + w * half + i % half;
-          ok = c < F;
-          n = (int64_t)(i / half) * F + c;
-        } else {
-          n = at.col * TN + r;
-          ok = n < F;
-        }
-        if (ok)
-          p = reinterpret_cast<const char*>(static_cast<const T*>(a.W) +
-                                            ((int64_t)at.e * a.d_out + n) * a.d_in);
+        n = at.col * TN + r;
+        ok = n < F;
       }
-      step[j] = p != nullptr ? RB : 0;
-      src[j] = p != nullptr ? p + chunk[j] : zero;
+      if constexpr (FAR) {
+        step[j] = ok ? RB : 0;
+        src[j] = ok ? (isA ? x : W) + n * kbytes + ch : reinterpret_cast<const char*>(zero_page);
+      } else {
+        off[j] = ok ? (uint32_t)n * (uint32_t)kbytes + ch : kOutOfRange;
+      }
     }
-    const int fr = lane & 31;
+    const int fr = lane % MI;
 #pragma unroll
-    for (int s = 0; s < kSlices; ++s) fs[s] = fr * RB + (((2 * s + (lane >> 5)) ^ swz(fr)) << 4);
-    fa = lds + wm * MB * 32 * RB;
-    fb = lds + TM * RB + wn * NB * 32 * RB;
+    for (int s = 0; s < kSlices; ++s)
+      fs[s] = fr * RB + (((s * (kSliceBytes / 16) + lane / MI) ^ swz(fr)) << 4);
+    fa = lds + wm * WR * RB;
+    fb = lds + TM * RB + wn * WC * RB;
   }
 
-  // Load j of the K step that starts `left` bytes before the end of K, into
-  // stage buffer `buf`.  Past the end (left <= 0) it keeps its place in the
-  // instruction stream and writes zeros into the wave's sink.
-  __device__ __forceinline__ void issue(int j, int buf, int left) {
+  // Load j of K step kt into stage buffer `buf`.  Past the end of K it writes
+  // zeros.
+  __device__ __forceinline__ void issue(int j, int buf, int kt) {
     const bool isA = j < kPwA;
-    const uint32_t dst = isA ? (wave * kPwA + j) * 1024 : TM * RB + (wave * kPwB + j - kPwA) * 1024;
-    const uint32_t to = left > 0 ? lds + buf * kStage + dst : lds + kMain + wave * 1024;
-    const char* p = chunk[j] < left ? src[j] : reinterpret_cast<const char*>(zero_page);
-    load_lds16(__builtin_amdgcn_readfirstlane(to), p);
-    src[j] += step[j];
+    const int blk = isA ? wave * kPwA + j : wave * kPwB + j - kPwA;
+    const uint32_t dst =
+        __builtin_amdgcn_readfirstlane(lds + buf * kStage + (isA ? 0 : TM * RB) + blk * 1024);
+    // uniform: the K step read (steps go round from k0), bytes left from there
+    const int k = kt + k0 < nk ? kt + k0 : kt + k0 - nk;
+    const int left = kt < nk ? kbytes - k * RB : 0;
+    // swz depends on the block's parity: known here where a wave has an even
+    // number of blocks, else from the wave
+    const int par = (isA ? kPwA : kPwB) % 2 == 0 ? (isA ? j : j - kPwA) & 1 : blk & 1;
+    const bool in = (RB == 64 ? chunk[0] : par ? chunk[1] : chunk[0]) < left;
+    if constexpr (FAR) {
+      load_lds16(dst, in ? src[j] : reinterpret_cast<const char*>(zero_page));
+      src[j] += step[j];
+    } else {
+      load_lds16(dst, isA ? xbuf : wbuf, in ? off[j] : kOutOfRange, k * RB);
+    }
   }
 
   __device__ __forceinline__ vec4u read16(uint32_t addr) const {
     return *reinterpret_cast<LDS_AS const vec4u*>((LDS_AS char*)(uintptr_t)addr);
   }
-  __device__ __forceinline__ void read_frag(Frags& f, int buf, int s, int i) const {
-    const uint32_t so = buf * kStage + fs[s];
-    if (i < MB) f.a[i] = read16(fa + so + i * 32 * RB);
-    else f.b[i - MB] = read16(fb + so + (i - MB) * 32 * RB);
+  __device__ __forceinline__ vec4u frag_a(int buf, int s, int i) const {
+    return read16(fa + buf * kStage + fs[s] + i * MI * RB);
+  }
+  __device__ __forceinline__ vec4u frag_b(int buf, int s, int i) const {
+    return read16(fb + buf * kStage + fs[s] + i * MI * RB);
   }
 
-  // The K loop.  In step kt (buffer S = kt % NS) the fragments of slice s + 1
-  // are read while slice s is multiplied.  Before the last slice one barrier:
-  // the next stage is in LDS (its loads are the oldest ones), and nobody
-  // reads buffer S any more; the loads of step kt + NS then go out between
-  // the products of the last slice and of the next step's first slices.
-  __device__ __forceinline__ void mainloop(f32x16 (&acc)[MB][NB]) {
+  // The K loop.  While slice s is multiplied, A row block by A row block, the
+  // fragments of slice s + 1 are read: A's into the registers that their row
+  // block has just left, B's into a second set.  Before the last slice one
+  // barrier: the next stage is in LDS (its loads are the oldest ones), and
+  // nobody reads buffer S any more; the loads of step kt + NS then go out
+  // between the products.
+  static constexpr int N = MB * NB;
+  static constexpr int kSpan = N * kSlices / 2;
+  __device__ __forceinline__ static constexpr int spread(int i, int n, int span) {   // items before slot i
+    return i >= span ? n : i * n / span;
+  }
+  template <int PAR>
+  __device__ __forceinline__ void round(int kt, int S, vec4u (&fa_)[MB], vec4u (&fb_)[2][NB],
+                                        Acc<MI> (&acc)[MB][NB]) {
+    const int SN = S + 1 == NS ? 0 : S + 1, SP = S == 0 ? NS - 1 : S - 1;
+    static_for<kSlices>([&](auto s_) __attribute__((always_inline)) {
+      constexpr int s = s_, cur = (s + PAR * kSlices) & 1;
+      constexpr bool last = s == kSlices - 1;
+      if (last) {
+        wait_loads_barrier<(NS - 2) * kLoads>();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      const int from = last ? SN : S;
+      constexpr int at = last ? 0 : s + 1;
+      __builtin_amdgcn_s_setprio(1);
+      static_for<N>([&](auto i_) __attribute__((always_inline)) {
+        constexpr int i = i_, a = i / NB, b = i % NB;
+        acc[a][b] = mfma<T, MI>(fb_[cur][b], fa_[a], acc[a][b]);
+        if constexpr (b == NB - 1) fa_[a] = frag_a(from, at, a);
+        // B fragments early, so that the next slice's first products have them
+        constexpr int q0 = spread(i, NB, N / 2), q1 = spread(i + 1, NB, N / 2);
+        static_for<q1 - q0>([&](auto q) __attribute__((always_inline)) {
+          fb_[cur ^ 1][q0 + q] = frag_b(from, at, q0 + q);
+        });
+        constexpr int slot = last ? i : (s + 1) * N + i;   // counted from the barrier
+        constexpr int l0 = spread(slot, kLoads, kSpan), l1 = spread(slot + 1, kLoads, kSpan);
+        static_for<l1 - l0>([&](auto q) __attribute__((always_inline)) {
+          if (last) issue(l0 + q, S, kt + NS);
+          else if (kt > 0) issue(l0 + q, SP, kt + NS - 1);
+        });
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      __builtin_amdgcn_s_setprio(0);
+    });
+  }
+  __device__ __forceinline__ void mainloop(Acc<MI> (&acc)[MB][NB]) {
 #pragma unroll
     for (int a = 0; a < MB; ++a)
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
+      for (int b = 0; b < NB; ++b) acc[a][b] = Acc<MI>{};
 #pragma unroll
     for (int d = 0; d < NS; ++d)
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) issue(j, d, kbytes - d * RB);
+      for (int j = 0; j < kLoads; ++j) issue(j, d, d);
     wait_loads_barrier<(NS - 1) * kLoads>();
-    Frags f[2];
+    vec4u fa_[MB], fb_[2][NB];
 #pragma unroll
-    for (int i = 0; i < MB + NB; ++i) read_frag(f[0], 0, 0, i);
-    constexpr int kHalf = (kLoads + 1) / 2;   // loads after the barrier; the rest a slice later
-    for (int kt = 0, S = 0; kt < nk; ++kt) {
-      const int SN = S + 1 == NS ? 0 : S + 1, SP = S == 0 ? NS - 1 : S - 1;
+    for (int i = 0; i < MB; ++i) fa_[i] = frag_a(0, 0, i);
 #pragma unroll
-      for (int s = 0; s < kSlices; ++s) {
-        const bool last = s == kSlices - 1;
-        if (last) {
-          wait_loads_barrier<(NS - 2) * kLoads>();
-          __builtin_amdgcn_sched_barrier(0);
-        }
-#pragma unroll
-        for (int i = 0; i < MB * NB; ++i) {
-          const int a = i / NB, b = i % NB;
-          acc[a][b] = mfma32<T>(f[s & 1].b[b], f[s & 1].a[a], acc[a][b]);
-          // spread over the products: the next slice's fragments, one load
-          for (int q = i * (MB + NB) / (MB * NB); q < (i + 1) * (MB + NB) / (MB * NB); ++q)
-            read_frag(f[(s + 1) & 1], last ? SN : S, last ? 0 : s + 1, q);
-          if (last) {
-            for (int q = i * kHalf / (MB * NB); q < (i + 1) * kHalf / (MB * NB); ++q)
-              issue(q, S, kbytes - (kt + NS) * RB);
-          } else if (s == 0 && kt > 0) {
-            for (int q = i * (kLoads - kHalf) / (MB * NB);
-                 q < (i + 1) * (kLoads - kHalf) / (MB * NB); ++q)
-              issue(kHalf + q, SP, kbytes - (kt + NS - 1) * RB);
-          }
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-      S = SN;
+    for (int i = 0; i < NB; ++i) fb_[0][i] = frag_b(0, 0, i);
+    int S = 0;
+    for (int kt = 0; kt < nk; kt += kUnroll) {
+      // where fragment sets alternate over two steps, one past the end
+      // multiplies zeros
+      static_for<kUnroll>([&](auto u) __attribute__((always_inline)) {
+        round<u>(kt + u, S, fa_, fb_, acc);
+        S = S + 1 == NS ? 0 : S + 1;
+      });
     }
     wait_loads_barrier<0>();   // the stages become the epilogue's staging
   }
@@ -323,10 +407,9 @@ struct Gemm {
   // rows leave in whole 16-byte pieces; bias, activation and residual in
   // float32, one rounding.
   static constexpr int UN = 16 / sizeof(T);   // values of a 16-byte piece
-  __device__ __forceinline__ uint32_t epi_off(int r, int c) const {   // c: 16-byte chunk
-    constexpr int cpr = NB * 8;
-    if constexpr (NB % 2 == 0) return r * NB * 128 + ((c ^ (r & 15)) << 4);
-    else return r * NB * 128 + ((c ^ ((r >> 1) & 7)) << 4);
+  __device__ __forceinline__ static uint32_t epi_off(int r, int c) {   // c: 16-byte chunk
+    if constexpr (WC % 64 == 0) return r * WC * 4 + ((c ^ (r & 15)) << 4);
+    else return r * WC * 4 + ((c ^ ((r >> 1) & 7)) << 4);
   }
   __device__ __forceinline__ void read_vals(uint32_t base, int r, int col, float (&v)[UN]) const {
 #pragma unroll
@@ -337,12 +420,12 @@ struct Gemm {
     }
   }
 
-  __device__ __forceinline__ void epilogue(const TileAt& at, const f32x16 (&acc)[MB][NB]) const {
+  __device__ __forceinline__ void epilogue(const TileAt& at, const Acc<MI> (&acc)[MB][NB]) const {
     const int F = GLU ? args.d_out / 2 : args.d_out;
-    constexpr int wave_cols = GLU ? NB * 16 : NB * 32;
+    constexpr int wave_cols = GLU ? WC / 2 : WC;
     constexpr int lanes = wave_cols / UN;    // lanes of one row
     constexpr int per = 64 / lanes;          // rows of one pass
-    const uint32_t base = lds + wave * NB * 4096;
+    const uint32_t base = lds + wave * WC * 128;
     const int c = (lane % lanes) * UN;
     const int col = at.col * kOut + wn * wave_cols + c;
     const bool col_ok = col < F;
@@ -354,69 +437,201 @@ struct Gemm {
       load_vals(bias + (int64_t)at.e * args.d_out + col, ba);
       if (GLU) load_vals(bias + (int64_t)at.e * args.d_out + F + col, bb);
     }
+    constexpr int G = 32 / MI;   // blocks of 32 rows
+    static_for<MB / G>([&](auto a_) __attribute__((always_inline)) {
+      constexpr int a = a_ * G;
+      const int r0 = wm * WR + a * MI;
+      if (r0 < at.rows) {   // wave-uniform
 #pragma unroll
-    for (int a = 0; a < MB; ++a) {
-      const int r0 = (wm * MB + a) * 32;
-      if (r0 >= at.rows) break;   // wave-uniform
+        for (int g = 0; g < G; ++g)
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+          for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int chunk16 = (b * 32 + 8 * g + 4 * (lane >> 5)) / 4;
-          f32x4 q;
+            for (int h = 0; h < MI * MI / 256; ++h) {   // register quads: 4 columns of one row
+              const int col4 = b * MI + (MI == 32 ? 8 * h + 4 * (lane / 32) : 4 * (lane / 16));
+              f32x4 q;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) q[i] = acc[a][b][4 * g + i];
-          *reinterpret_cast<LDS_AS f32x4*>(
-              (LDS_AS char*)(uintptr_t)(base + epi_off(lane & 31, chunk16))) = q;
-        }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      for (int p = 0; p < 32 / per; ++p) {
-        const int r = p * per + lane / lanes;
-        if (r0 + r < at.rows && col_ok) {
-          const int64_t o = (at.lo + r0 + r) * F + col;
-          float z[UN], v[UN];
-          read_vals(base, r, c, z);
+              for (int i = 0; i < 4; ++i) q[i] = acc[a + g][b][4 * h + i];
+              *reinterpret_cast<LDS_AS f32x4*>(
+                  (LDS_AS char*)(uintptr_t)(base + epi_off(g * MI + lane % MI, col4 / 4))) = q;
+            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        for (int p = 0; p < 32 / per; ++p) {
+          const int r = p * per + lane / lanes;
+          if (r0 + r < at.rows && col_ok) {
+            const int64_t o = (at.lo + r0 + r) * F + col;
+            float z[UN], v[UN];
+            read_vals(base, r, c, z);
 #pragma unroll
-          for (int i = 0; i < UN; ++i) z[i] += ba[i];
-          if (args.pre_a != nullptr) store_vals(static_cast<T*>(args.pre_a) + o, z);
-          if constexpr (GLU) {
-            float w[UN];
-            read_vals(base, r, NB * 16 + c, w);
+            for (int i = 0; i < UN; ++i) z[i] += ba[i];
+            if (args.pre_a != nullptr) store_vals(static_cast<T*>(args.pre_a) + o, z);
+            if constexpr (GLU) {
+              float w[UN];
+              read_vals(base, r, WC / 2 + c, w);
 #pragma unroll
-            for (int i = 0; i < UN; ++i) w[i] += bb[i];
-            if (args.pre_b != nullptr) store_vals(static_cast<T*>(args.pre_b) + o, w);
+              for (int i = 0; i < UN; ++i) w[i] += bb[i];
+              if (args.pre_b != nullptr) store_vals(static_cast<T*>(args.pre_b) + o, w);
 #pragma unroll
-            for (int i = 0; i < UN; ++i) v[i] = z[i] * sigmoid_f32(z[i]) * w[i];
-          } else {
+              for (int i = 0; i < UN; ++i) v[i] = z[i] * sigmoid_f32(z[i]) * w[i];
+            } else {
 #pragma unroll
-            for (int i = 0; i < UN; ++i) v[i] = activate(args.act, z[i]);
+              for (int i = 0; i < UN; ++i) v[i] = activate(args.act, z[i]);
+            }
+            if (args.residual != nullptr) {
+              float r8[UN];
+              load_vals(static_cast<const T*>(args.residual) + o, r8);
+#pragma unroll
+              for (int i = 0; i < UN; ++i) v[i] += r8[i];
+            }
+            store_vals(static_cast<T*>(args.y) + o, v);
           }
-          if (args.residual != nullptr) {
-            float r8[UN];
-            load_vals(static_cast<const T*>(args.residual) + o, r8);
-#pragma unroll
-            for (int i = 0; i < UN; ++i) v[i] += r8[i];
-          }
-          store_vals(static_cast<T*>(args.y) + o, v);
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-    }
+    });
   }
 };
 
 template <typename G>
 __global__ __launch_bounds__(G::kThreads, G::kWavesPerSimd) void gemm_kernel(ForwardArgs args,
-                                                                             int cols, int group) {
+                                                                             int cols) {
   __shared__ __attribute__((aligned(16))) char smem[G::kLds];
   TileAt at;
-  if (!find_tile(args.seg, args.E, args.P, G::TM, cols, group, at)) return;
+  if (!find_tile(args.seg, args.E, args.P, G::TM, cols, at)) return;
   G g(args, at, (LDS_AS char*)smem);
-  f32x16 acc[G::kMB][G::kNB];
+  Acc<G::kMI> acc[G::kMB][G::kNB];
   g.mainloop(acc);
   g.epilogue(at, acc);
+}
+
+// ---- 256-row tiles, ragged ends and the last round
+// Tiles of 256 rows with one workgroup a CU: the ends of the segments get
+// 128-row or 64-row code (an expert's last tile is half empty on average), and
+// the last round of an XCD's 32 CUs, if it would fill half of them or fewer, is
+// cut into 128-row or 64-row parts.  Whole tiles come first, then the ends,
+// each list in eighths over the XCDs.
+constexpr int kXcds = 8, kXcdCus = 32;
+
+__device__ __forceinline__ bool find_ragged_tile(const int32_t* seg, int E, int64_t P, int cols,
+                                                 TileAt& at) {
+  const int lane = threadIdx.x & 63;
+  int64_t off[5];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) {
+    const int e = 4 * lane + j;
+    const int64_t o = seg[e < E ? e : E];
+    off[j] = o < 0 ? 0 : o > P ? P : o;
+  }
+  // One round of 128-row tiles reads W at the rate of memory and ends sooner
+  // than 256-row tiles on part of the CUs; else 256-row tiles.
+  int halves = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (off[j + 1] > off[j]) halves += (int)((off[j + 1] - off[j] + 127) / 128);
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) halves += __shfl_xor(halves, m, 64);
+  const int tm =
+      (int64_t)__builtin_amdgcn_readfirstlane(halves) * cols <= kXcds * kXcdCus ? 128 : 256;
+  int n[4], full = 0, part = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    n[j] = off[j + 1] > off[j] ? (int)(off[j + 1] - off[j]) : 0;
+    full += n[j] / tm;
+    part += n[j] % tm != 0;
+  }
+  int fend = full, pend = part;   // whole tiles and ends up to this lane's experts
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const int f = __shfl_up(fend, m, 64), q = __shfl_up(pend, m, 64);
+    if (lane >= m) {
+      fend += f;
+      pend += q;
+    }
+  }
+  const int fulls = __builtin_amdgcn_readlane(fend, 63);
+  const int parts = __builtin_amdgcn_readlane(pend, 63);
+  const int x = blockIdx.x % kXcds;
+  const int64_t pos = blockIdx.x / kXcds;
+  const int64_t f0 = (int64_t)fulls * cols * x / kXcds, f1 = (int64_t)fulls * cols * (x + 1) / kXcds;
+  const int64_t p0 = (int64_t)parts * cols * x / kXcds, p1 = (int64_t)parts * cols * (x + 1) / kXcds;
+  const int64_t mine = f1 - f0 + p1 - p0;
+  const int64_t rounds = mine / kXcdCus * kXcdCus;
+  const int rem = (int)(mine - rounds);
+  int64_t tile = pos;
+  int piece = 0, cut = 1;
+  if (pos >= rounds) {
+    cut = rem * 4 <= kXcdCus ? 4 : rem * 2 <= kXcdCus ? 2 : 1;
+    if (pos - rounds >= (int64_t)rem * cut) return false;
+    const int q = (int)(pos - rounds);
+    tile = rounds + q / cut;
+    piece = q % cut;
+  }
+  const bool whole = tile < f1 - f0;
+  int r;   // row tile in its list
+  if (whole) {
+    const int64_t t = f0 + tile, per = (int64_t)kGroup * cols;
+    const int g = (int)(t / per), in = (int)(t - g * per);
+    const int left = fulls - g * kGroup, gr = left < kGroup ? left : kGroup;
+    r = g * kGroup + in % gr;
+    at.col = in / gr;
+  } else {
+    const int64_t t = p0 + tile - (f1 - f0);
+    r = (int)(t / cols);
+    at.col = (int)(t - (int64_t)r * cols);
+  }
+  r = __builtin_amdgcn_readfirstlane(r);
+  at.col = __builtin_amdgcn_readfirstlane(at.col);
+  const int owner =
+      __ffsll((unsigned long long)(whole ? __ballot(fend > r) : __ballot(pend > r))) - 1;
+  int sub = whole ? r - (fend - full) : r - (pend - part), j = 0;   // meant for the owner lane
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int c = whole ? n[i] / tm : (int)(n[i] % tm != 0);
+    if (j == i && sub >= c) {
+      sub -= c;
+      j = i + 1;
+    }
+  }
+  const int nj = j == 0 ? n[0] : j == 1 ? n[1] : j == 2 ? n[2] : n[3];
+  const int64_t oj = j == 0 ? off[0] : j == 1 ? off[1] : j == 2 ? off[2] : off[3];
+  const int first = (whole ? sub : nj / tm) * tm + piece * (tm / cut);
+  int rows = nj - first;
+  if (rows > tm / cut) rows = tm / cut;
+  at.e = __builtin_amdgcn_readlane(4 * lane + j, owner);
+  at.lo = (uint32_t)__builtin_amdgcn_readlane((uint32_t)(oj + first), owner);   // P < 2^31
+  at.rows = __builtin_amdgcn_readlane(rows, owner);
+  return at.rows > 0;
+}
+
+template <typename G>
+__device__ __forceinline__ void run_tile(const ForwardArgs& args, const TileAt& at,
+                                         LDS_AS char* smem) {
+  G g(args, at, smem);
+  Acc<G::kMI> acc[G::kMB][G::kNB];
+  g.mainloop(acc);
+  g.epilogue(at, acc);
+}
+
+template <typename T, bool GLU>
+struct Ragged {
+  typedef Gemm<T, 16, 128, 64, 2, 4, 128, 2, GLU> G256;
+  typedef Gemm<T, 16, 64, 64, 2, 4, 128, 3, GLU> G128;
+  typedef Gemm<T, 16, 32, 64, 2, 4, 128, 3, GLU> G64;
+  static constexpr int kLds = std::max(std::max(G256::kLds, G128::kLds), G64::kLds);
+  static constexpr int kThreads = G256::kThreads, kOut = G256::kOut;
+};
+
+template <typename T, bool GLU>
+__global__ __launch_bounds__(512, 2) void ragged_gemm_kernel(ForwardArgs args, int cols) {
+  typedef Ragged<T, GLU> R;
+  __shared__ __attribute__((aligned(16))) char smem[R::kLds];
+  TileAt at;
+  if (!find_ragged_tile(args.seg, args.E, args.P, cols, at)) return;
+  if (at.rows > 128) run_tile<typename R::G256>(args, at, (LDS_AS char*)smem);
+  else if (at.rows > 64) run_tile<typename R::G128>(args, at, (LDS_AS char*)smem);
+  else run_tile<typename R::G64>(args, at, (LDS_AS char*)smem);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -425,11 +640,11 @@ __global__ __launch_bounds__(G::kThreads, G::kWavesPerSimd) void gemm_kernel(For
 // operands straight into fragments (no LDS, nothing is reused), partial sums
 // meet in LDS.
 template <typename T, int NC, bool GLU>
-__global__ __launch_bounds__(256) void few_rows_kernel(ForwardArgs args, int cols, int group) {
+__global__ __launch_bounds__(256) void few_rows_kernel(ForwardArgs args, int cols) {
   constexpr int kOut = GLU ? NC * 8 : NC * 16;
   __shared__ float part[4][16][NC * 16 + 4];
   TileAt at;
-  if (!find_tile(args.seg, args.E, args.P, 16, cols, group, at)) return;
+  if (!find_tile(args.seg, args.E, args.P, 16, cols, at)) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int F = GLU ? args.d_out / 2 : args.d_out;
@@ -482,7 +697,7 @@ __global__ __launch_bounds__(256) void few_rows_kernel(ForwardArgs args, int col
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int c = 0; c < NC; ++c) acc[c] = mfma16<T>(w[u][c], x[u], acc[c]);
+      for (int c = 0; c < NC; ++c) acc[c] = mfma<T, 16>(w[u][c], x[u], acc[c]);
 #pragma unroll
     for (int c = 0; c < NC; ++c) wp[c] += U * wstep[c];
     xp += U * xstep;
@@ -493,7 +708,7 @@ __global__ __launch_bounds__(256) void few_rows_kernel(ForwardArgs args, int col
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const vec4u w = *reinterpret_cast<const vec4u*>(in ? wp[c] : zero);
-      acc[c] = mfma16<T>(w, x, acc[c]);
+      acc[c] = mfma<T, 16>(w, x, acc[c]);
       wp[c] += wstep[c];
     }
     xp += xstep;
@@ -543,12 +758,26 @@ int64_t grid_blocks(int64_t P, int E, int tm, int64_t cols) {
 }
 
 template <typename G>
-hipError_t launch_gemm(const ForwardArgs& a, int F, int group, hipStream_t s) {
+hipError_t launch_gemm(const ForwardArgs& a, int F, hipStream_t s) {
   const int cols = (F + G::kOut - 1) / G::kOut;
   const int64_t blocks = grid_blocks(a.P, a.E, G::TM, cols);
   if (blocks * G::kThreads >= int64_t(1) << 32) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(gemm_kernel<G>, dim3((uint32_t)blocks), dim3(G::kThreads), 0, s, a, cols,
-                     group);
+  hipLaunchKernelGGL(gemm_kernel<G>, dim3((uint32_t)blocks), dim3(G::kThreads), 0, s, a, cols);
+  return hipGetLastError();
+}
+
+template <typename T, bool GLU>
+hipError_t launch_ragged(const ForwardArgs& a, int F, hipStream_t s) {
+  typedef Ragged<T, GLU> R;
+  const int cols = (F + R::kOut - 1) / R::kOut;
+  // most tiles of an XCD: its share of the whole tiles and of the ends, and
+  // the parts of a cut round
+  const int64_t ends = a.P < a.E ? a.P : a.E;
+  const int64_t most = a.P / 256 * cols / kXcds + ends * cols / kXcds + 2 + kXcdCus;
+  const int64_t blocks = most * kXcds;
+  if (blocks * R::kThreads >= int64_t(1) << 32) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((ragged_gemm_kernel<T, GLU>), dim3((uint32_t)blocks), dim3(R::kThreads), 0, s,
+                     a, cols);
   return hipGetLastError();
 }
 
@@ -559,22 +788,53 @@ hipError_t launch_few_rows(const ForwardArgs& a, int F, hipStream_t s) {
   const int64_t blocks = grid_blocks(a.P, a.E, 16, cols);
   if (blocks * 256 >= int64_t(1) << 32) return hipErrorInvalidValue;
   hipLaunchKernelGGL((few_rows_kernel<T, NC, GLU>), dim3((uint32_t)blocks), dim3(256), 0, s, a,
-                     cols, 8);
+                     cols);
   return hipGetLastError();
 }
 
-template <bool GLU>
-hipError_t forward_bf16(const ForwardArgs& a, int F, hipStream_t s) {
-  const int64_t mean = a.P / a.E;
-  if (mean <= 8) return launch_few_rows<uint16_t, 2, GLU>(a, F, s);
-  if (mean < 256) return launch_gemm<Gemm<uint16_t, 2, 4, 2, 2, 64, 3, GLU>>(a, F, 4, s);
-  return launch_gemm<Gemm<uint16_t, 4, 4, 2, 2, 64, 4, GLU>>(a, F, 8, s);
+// Workgroups that a call is expected to have with tiles of tm rows and `out`
+// columns: the segments live on the device, so half of the experts are taken
+// to end in a tile of their own.
+int64_t expected(const ForwardArgs& a, int F, int tm, int out) {
+  const int64_t ends = a.P < a.E ? a.P : a.E;
+  const int64_t tiles = std::max(ends, a.P / tm + ends / 2);
+  return tiles * ((F + out - 1) / out);
 }
 
+// The smallest tiles whose workgroups the 256 CUs hold at once, or nearly:
+// below that a product takes the time of one workgroup's walk over K, which
+// grows with the tile; above it the operands' re-reads count.  Measured (us;
+// W of 2048 columns and 1536 rows an expert, SwiGLU): 1 expert, 64 rows: 10.2
+// without tiles, 12.3 with 32x64, 16.6 with 64x128, 34 with 256x256; 4
+// experts, 64 rows each: 25.1, 13.3, 16.9, 34; 4 experts, 512 rows each: 147,
+// 41, 24, 23; 16 experts, 512 rows each: 542, 149, 95, 71.
+template <typename T, bool GLU>
+hipError_t forward_bf16(const ForwardArgs& a, int F, bool far, hipStream_t s) {
+  constexpr int h = GLU ? 2 : 1;   // W rows of an output column
+  if (expected(a, F, 16, 32 / h) <= 320) return launch_few_rows<T, 2, GLU>(a, F, s);
+  if (far) return launch_gemm<Gemm<T, 16, 32, 64, 2, 2, 128, 3, GLU, true>>(a, F, s);
+  // few rows for much W: wide tiles keep more of W in flight (16 experts of
+  // 4096 columns and 2816 rows, 8 rows each: 67 us, 76 with the tiles below)
+  if (a.P <= (int64_t)16 * a.E && expected(a, F, 32, 256 / h) >= 160)
+    return launch_gemm<Gemm<T, 16, 32, 64, 1, 4, 128, 4, GLU>>(a, F, s);
+  if (expected(a, F, 32, 64 / h) <= 320)
+    return launch_gemm<Gemm<T, 16, 32, 32, 1, 2, 128, 4, GLU>>(a, F, s);
+  if (expected(a, F, 64, 64 / h) <= 400)
+    return launch_gemm<Gemm<T, 16, 32, 32, 2, 2, 128, 3, GLU>>(a, F, s);
+  if (expected(a, F, 64, 128 / h) <= 512)
+    return launch_gemm<Gemm<T, 16, 32, 64, 2, 2, 128, 3, GLU>>(a, F, s);
+  return launch_ragged<T, GLU>(a, F, s);
+}
+
+// float32 products are bound by the matrix units (a sixteenth of bf16's rate)
+// from some 16 rows an expert on, so small tiles that spread evenly win
+// throughout: 8 experts, 512 rows each, 768 columns and 2048 rows of W: 126 us
+// with 64x64, 173 with 128x128, 216 with 256-row tiles.
 template <bool GLU>
-hipError_t forward_f32(const ForwardArgs& a, int F, hipStream_t s) {
-  if (a.P / a.E <= 8) return launch_few_rows<float, 2, GLU>(a, F, s);
-  return launch_gemm<Gemm<float, 2, 2, 2, 2, 128, 2, GLU>>(a, F, 8, s);
+hipError_t forward_f32(const ForwardArgs& a, int F, bool far, hipStream_t s) {
+  if (expected(a, F, 16, GLU ? 16 : 32) <= 800) return launch_few_rows<float, 2, GLU>(a, F, s);
+  if (far) return launch_gemm<Gemm<float, 16, 32, 32, 2, 2, 128, 2, GLU, true>>(a, F, s);
+  return launch_gemm<Gemm<float, 16, 32, 32, 2, 2, 128, 2, GLU>>(a, F, s);
 }
 
 }  // namespace
@@ -583,8 +843,15 @@ hipError_t launch_grouped_forward(int dtype, const ForwardArgs& a, hipStream_t s
   if (a.P == 0) return hipSuccess;
   const bool glu = a.act == LRMOE_ACT_SWIGLU;
   const int F = glu ? a.d_out / 2 : a.d_out;
-  if (dtype == LRMOE_BF16) return glu ? forward_bf16<true>(a, F, s) : forward_bf16<false>(a, F, s);
-  return glu ? forward_f32<true>(a, F, s) : forward_f32<false>(a, F, s);
+  // beyond a buffer's reach: one expert's weights, or x where its rows are
+  // picked by index
+  const int64_t kbytes = (int64_t)a.d_in * (dtype == LRMOE_BF16 ? 2 : 4);
+  const bool far = a.d_out * kbytes >= kNearBytes ||
+                   (a.row_index != nullptr && a.T * kbytes >= kNearBytes);
+  if (dtype == LRMOE_BF16)
+    return glu ? forward_bf16<uint16_t, true>(a, F, far, s)
+               : forward_bf16<uint16_t, false>(a, F, far, s);
+  return glu ? forward_f32<true>(a, F, far, s) : forward_f32<false>(a, F, far, s);
 }
 
 }  // namespace lrmoe

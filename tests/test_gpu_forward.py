@@ -369,6 +369,79 @@ def test_linear_shapes(seg, d_in, d_out, dt):
     check_linear(seg, x, W, row, bias, res, "none", False)
 
 
+def zipf_seg(P, E):
+    w = torch.arange(1, E + 1).double() ** -0.8
+    ends = (P * torch.cumsum(w, 0) / w.sum()).round().long().tolist()
+    return [0] + ends[:-1] + [P]
+
+
+# (segments, columns of y): each of the launch's tile shapes, by the workgroups
+# that the call is expected to have
+SHAPES = {
+    "32x256": (zipf_seg(512, 64), 776), "32x64": (zipf_seg(300, 4), 1032),
+    "64x64": (zipf_seg(1200, 4), 1032), "64x128": (zipf_seg(2500, 4), 1032),
+    # 256-row tiles; 128-row ones where they fill one round; whole tiles, ends
+    # of each class, and last rounds cut in four, in two and not at all
+    "one round of 128": ([0, 4090], 1032), "whole and ends": ([0, 1500, 1501, 1700, 4200], 2056),
+    "cut in four": ([0, 4100, 8200], 2304), "cut in two": ([0, 9990], 2304),
+}
+
+
+@pytest.mark.parametrize("shape", list(SHAPES))
+@pytest.mark.parametrize("name,d_in", [("none", 40), ("swiglu", 136)])
+def test_linear_tile_shapes(shape, name, d_in):
+    seg, F = SHAPES[shape]
+    F = F // 16 * 8 if name == "swiglu" else F
+    x, W, row, bias, _ = linear_inputs(seg, d_in, 2 * F if name == "swiglu" else F, BF16, 77,
+                                       name=name)
+    check_linear(seg, x, W, row, bias, None, name, name == "swiglu")
+
+
+@pytest.mark.parametrize("name", ["gelu", "swiglu"])
+@pytest.mark.parametrize("seg", [zipf_seg(900, 4), [0, 700]], ids=str)
+def test_linear_float32_tiles(name, seg):
+    x, W, row, bias, res = linear_inputs(seg, 100, 1224, F32, 78, name=name)
+    check_linear(seg, x, W, row, bias, res, name, True)
+
+
+@pytest.mark.parametrize("dt,T", [(BF16, 1_100_000), (F32, 550_000)])
+def test_linear_tiles_of_rows_beyond_32_bits(dt, T):
+    """Picked rows of an x beyond a buffer's 2 GiB, in tiles (300 rows, many
+    columns); also an index out of range."""
+    d_in, F, n = 2048, 2056, 300
+    x = torch.zeros((T, d_in), dtype=dt, device=DEV)
+    tail = normal(gen(6), (n, d_in), dt)
+    x[T - n:] = tail.to(DEV)
+    W = normal(gen(7), (1, F, d_in), dt, 0.1)
+    row = torch.arange(T - n, T, dtype=torch.int32, device=DEV)
+    row[5], row[250] = T, -3
+    tail[5] = tail[250] = 0
+    y = L.grouped_forward(torch.tensor([0, n], dtype=torch.int32, device=DEV), x, W.to(DEV),
+                          row_index=row)["y"]
+    ref = O.linear([0, n], tail, W)
+    ez = (d_in + 2) * 2 * U * ref["mag"]
+    within(y, ref["y"], ez + HALF[dt] * (ref["y"].abs() + ez), "y")
+
+
+def test_linear_rows_in_any_batch_company():
+    """NaN rows of one expert or token touch no other row."""
+    seg = zipf_seg(2500, 4)
+    x, W, row, _, _ = linear_inputs(seg, 72, 1032, BF16, 79)
+    x[3] = float("nan")
+    W[1, 5] = float("inf")
+    put = lambda t: t.to(DEV)   # noqa: E731
+    s = torch.tensor(seg, dtype=torch.int32, device=DEV)
+    y = L.grouped_forward(s, put(x), put(W), row_index=put(row))["y"].float().cpu()
+    e = torch.bucketize(torch.arange(2500), torch.tensor(seg[1:]), right=True)
+    bad_row = row == 3
+    assert torch.isnan(y[bad_row]).all()
+    rest = y[~bad_row]
+    inf_col = torch.zeros_like(y, dtype=torch.bool)
+    inf_col[e == 1, 5] = True
+    assert torch.isfinite(rest[~inf_col[~bad_row]]).all()
+    assert not torch.isfinite(rest[inf_col[~bad_row]]).any()
+
+
 @pytest.mark.parametrize("name", list(ACTS))
 @pytest.mark.parametrize("seg", [[0, 2, 9], [0, 33, 33, 150], [0, 270, 530]], ids=str)
 @pytest.mark.parametrize("dt", [BF16, F32])
