@@ -9,9 +9,9 @@
 //   GELU'(a) = Phi(a) + a phi(a)
 //
 // Memory bound: dy, a (and b) are read once, dz written once.  A workgroup
-// takes a run of kRows rows of one expert and 64 * N columns; its four waves
-// take every fourth row and keep the column sums in registers, which meet in
-// LDS and go to the workspace, one row of sums for each run.  A second kernel
+// takes a run of kRows rows of one expert and LPR lanes' columns, its groups of
+// LPR lanes take a row each in turn and keep the column sums in registers,
+// which meet in LDS and go to the workspace, one row of sums for each run.  A second kernel
 // adds an expert's runs in order, so the sums do not depend on timing.
 #include "forward.h"
 
@@ -19,8 +19,8 @@ namespace lrmoe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWaves = 4;
 constexpr int kRows = 64;
+constexpr int kBatch = 2;
 
 // Runs of an expert with n rows.
 __host__ __device__ inline int64_t runs_of(int64_t n) { return (n + kRows - 1) / kRows; }
@@ -77,25 +77,25 @@ __device__ __forceinline__ float act_grad(float a) {
   if constexpr (ACT == LRMOE_ACT_RELU) return a > 0.f ? 1.f : 0.f;
   if constexpr (ACT == LRMOE_ACT_SILU || ACT == LRMOE_ACT_SWIGLU) {
     const float s = sigmoid_f32(a);
-    return s * (1.f + a * (1.f - s));
+    return s + a * s * (1.f - s);
   }
   if constexpr (ACT == LRMOE_ACT_GELU)
-    return 0.5f * (1.f + erff(a * 0.70710678f)) + a * (0.39894228f * expf(-0.5f * a * a));
+    return 0.5f * (1.f + erff(a * 0.70710678f)) + a * (0.39894228f * __builtin_amdgcn_exp2f(-0.72134752f * a * a));
   return 1.f;
 }
 
-template <typename T, typename TO, int N, int ACT>
+template <typename T, typename TO, int N, int ACT, int LPR>
 __global__ __launch_bounds__(kThreads) void act_backward_kernel(
     const int32_t* __restrict__ seg, const T* __restrict__ dy, const T* __restrict__ pa,
     const T* __restrict__ pb, int64_t P, int E, int F, TO* __restrict__ dz,
     float* __restrict__ sums, int pieces) {
   constexpr bool GLU = ACT == LRMOE_ACT_SWIGLU;
   constexpr int H = GLU ? 2 : 1;
-  __shared__ float part[kWaves - 1][H * N][64];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  constexpr int kGroups = kThreads / LPR;   // rows at a time
+  __shared__ float part[kGroups - 1][H * N][LPR];
+  const int tid = threadIdx.x, lane = tid % LPR, group = tid / LPR;
   const int64_t run = blockIdx.x / pieces;
-  const int col = (int)(blockIdx.x % pieces) * (64 * N) + lane * N;
+  const int col = (int)(blockIdx.x % pieces) * (LPR * N) + lane * N;
   int e;
   int64_t sub;
   if (!find_run(seg, E, P, run, e, sub)) return;   // the same answer in every wave
@@ -108,49 +108,61 @@ __global__ __launch_bounds__(kThreads) void act_backward_kernel(
   for (int h = 0; h < H; ++h)
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[h][i] = 0.f;
-  if (col < F)
-#pragma unroll 2
-    for (int64_t u = lo + wave; u < hi; u += kWaves) {
-      float g[N], a[N], b[N];
-      load_vals(dy + u * F + col, g);
-      if (ACT != LRMOE_ACT_NONE) load_vals(pa + u * F + col, a);
-      if (GLU) load_vals(pb + u * F + col, b);
-      float z[H][N];
+  if (col < F) {
+    // kBatch rows in flight: their loads go out before the first is used
+    for (int64_t u0 = lo + group; u0 < hi; u0 += kBatch * kGroups) {
+      float g[kBatch][N], a[kBatch][N], b[kBatch][N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if constexpr (GLU) {
-          const float s = sigmoid_f32(a[i]);
-          z[0][i] = g[i] * b[i] * (s * (1.f + a[i] * (1.f - s)));
-          z[H - 1][i] = g[i] * (a[i] * s);
-        } else if constexpr (ACT == LRMOE_ACT_RELU) {
-          z[0][i] = a[i] > 0.f ? g[i] : 0.f;
-        } else if constexpr (ACT == LRMOE_ACT_NONE) {
-          z[0][i] = g[i];
-        } else {
-          z[0][i] = g[i] * act_grad<ACT>(a[i]);
+      for (int k = 0; k < kBatch; ++k) {
+        const int64_t u = u0 + k * kGroups;
+        if (u < hi) {
+          load_vals(dy + u * F + col, g[k]);
+          if (ACT != LRMOE_ACT_NONE) load_vals(pa + u * F + col, a[k]);
+          if (GLU) load_vals(pb + u * F + col, b[k]);
         }
       }
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
-        store_vals(dz + (u * H + h) * F + col, z[h]);
+      for (int k = 0; k < kBatch; ++k) {
+        const int64_t u = u0 + k * kGroups;
+        if (u >= hi) break;
+        float z[H][N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[h][i] += z[h][i];
+        for (int i = 0; i < N; ++i) {
+          if constexpr (GLU) {
+            const float s = sigmoid_f32(a[k][i]), as = a[k][i] * s;
+            z[0][i] = g[k][i] * b[k][i] * (s + as * (1.f - s));
+            z[H - 1][i] = g[k][i] * as;
+          } else if constexpr (ACT == LRMOE_ACT_RELU) {
+            z[0][i] = a[k][i] > 0.f ? g[k][i] : 0.f;
+          } else if constexpr (ACT == LRMOE_ACT_NONE) {
+            z[0][i] = g[k][i];
+          } else {
+            z[0][i] = g[k][i] * act_grad<ACT>(a[k][i]);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          store_vals(dz + (u * H + h) * F + col, z[h]);
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[h][i] += z[h][i];
+        }
       }
     }
+  }
   if (sums == nullptr) return;
-  if (wave > 0)
+  if (group > 0)
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
-      for (int i = 0; i < N; ++i) part[wave - 1][h * N + i][lane] = acc[h][i];
+      for (int i = 0; i < N; ++i) part[group - 1][h * N + i][lane] = acc[h][i];
   __syncthreads();
-  if (wave == 0 && col < F) {
+  if (group == 0 && col < F) {
 #pragma unroll
     for (int h = 0; h < H; ++h) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int w = 0; w < kWaves - 1; ++w) acc[h][i] += part[w][h * N + i][lane];
+        for (int w = 0; w < kGroups - 1; ++w) acc[h][i] += part[w][h * N + i][lane];
       store_vals(sums + (run * H + h) * F + col, acc[h]);
     }
   }
@@ -181,19 +193,19 @@ __global__ __launch_bounds__(kThreads) void dbias_kernel(const int32_t* __restri
   dbias[(int64_t)e * width + col] = s;
 }
 
-template <typename T, typename TO, int N>
+template <typename T, typename TO, int N, int LPR>
 hipError_t run(int act, const int32_t* seg, const void* dy, const void* a, const void* b, int64_t P,
                int E, int F, void* dz, float* sums, hipStream_t s) {
-  const int pieces = (F + 64 * N - 1) / (64 * N);
+  const int pieces = (F + LPR * N - 1) / (LPR * N);
   const int64_t blocks = max_runs(P, E) * pieces;
   if (blocks == 0) return hipSuccess;
   if (blocks >= int64_t(1) << 24) return hipErrorInvalidValue;   // 2^32 threads
   const dim3 grid((uint32_t)blocks), block(kThreads);
-#define LRMOE_ACT(A)                                                                            \
-  case A:                                                                                       \
-    hipLaunchKernelGGL((act_backward_kernel<T, TO, N, A>), grid, block, 0, s, seg,              \
-                       static_cast<const T*>(dy), static_cast<const T*>(a),                     \
-                       static_cast<const T*>(b), P, E, F, static_cast<TO*>(dz), sums, pieces);  \
+#define LRMOE_ACT(A)                                                                               \
+  case A:                                                                                          \
+    hipLaunchKernelGGL((act_backward_kernel<T, TO, N, A, LPR>), grid, block, 0, s, seg,            \
+                       static_cast<const T*>(dy), static_cast<const T*>(a),                        \
+                       static_cast<const T*>(b), P, E, F, static_cast<TO*>(dz), sums, pieces);     \
     break
   switch (act) {
     LRMOE_ACT(LRMOE_ACT_NONE);
@@ -204,6 +216,19 @@ hipError_t run(int act, const int32_t* seg, const void* dy, const void* a, const
   }
 #undef LRMOE_ACT
   return hipGetLastError();
+}
+
+// Lanes of a row: as many as leave the fewest of them past its end (768 bf16
+// columns: 64 lanes would idle in a quarter of their steps, 32 in none).
+template <typename T, typename TO, int N>
+hipError_t run(int act, const int32_t* seg, const void* dy, const void* a, const void* b, int64_t P,
+               int E, int F, void* dz, float* sums, hipStream_t s) {
+  const int units = (F + N - 1) / N;
+  const int w64 = (units + 63) / 64 * 64, w32 = (units + 31) / 32 * 32;
+  const int w16 = (units + 15) / 16 * 16;
+  if (w64 <= w32) return run<T, TO, N, 64>(act, seg, dy, a, b, P, E, F, dz, sums, s);
+  if (w32 <= w16) return run<T, TO, N, 32>(act, seg, dy, a, b, P, E, F, dz, sums, s);
+  return run<T, TO, N, 16>(act, seg, dy, a, b, P, E, F, dz, sums, s);
 }
 
 }  // namespace

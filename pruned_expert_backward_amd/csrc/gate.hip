@@ -25,11 +25,14 @@
 // underflow below -103.
 //
 // Mapping: LANES lanes own one row, V values each.  Rows of up to 256 experts
-// and 16 slots take 16 lanes, so a wave works on four rows and the argmax
-// needs four exchange steps instead of six; wider ones take the whole wave.
-// The K rounds are a running argmax over registers: no LDS, no sorting.  The
-// choice with a selection bias compares float64 keys, since the order of two
-// near values decides a whole number.
+// and 16 slots take 16 lanes, so a wave works on four rows and an exchange is
+// four DPP instructions; wider ones take the whole wave.  The K rounds are a
+// running argmax over registers: no LDS, no sorting (keys and experts packed
+// into float64 numbers and sorted per lane were 1.7 to 4 times slower).  The order
+// of two near keys decides a whole number, so with a selection bias it is float64's; but
+// float64 sigmoids of every logit cost more than all else, so float32 keys
+// choose first, and where neighbours among the best are within the float32
+// error (one row in a thousand) their float64 keys put them in order.
 #include <algorithm>
 #include <type_traits>
 
@@ -93,22 +96,170 @@ __device__ __forceinline__ void load_row(const T* row, int E, int l, float (&x)[
   }
 }
 
-template <int LANES>
-__device__ __forceinline__ float group_sum(float x) {
-#pragma unroll
-  for (int m = 1; m < LANES; m <<= 1) x += __shfl_xor(x, m, LANES);
-  return x;
+// The value of the lane that step S of an exchange over LANES lanes pairs this
+// one with.  After steps 0 .. S every lane of a run of 2^(S + 1) has the run's
+// result: inside a row of 16 lanes by DPP (neighbours, pairs, the mirrored
+// half row, the mirrored row), across rows through the LDS crossbar.
+template <int S>
+__device__ __forceinline__ int partner(int x) {
+  if constexpr (S == 0) return __builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, true);        // 1 0 3 2
+  else if constexpr (S == 1) return __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, true);   // 2 3 0 1
+  else if constexpr (S == 2) return __builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, true);
+  else if constexpr (S == 3) return __builtin_amdgcn_mov_dpp(x, 0x140, 0xF, 0xF, true);
+  else return __shfl_xor(x, 1 << S, 64);
 }
-template <int LANES>
+template <int S>
+__device__ __forceinline__ float partner(float x) {
+  return __int_as_float(partner<S>(__float_as_int(x)));
+}
+template <int S>
+__device__ __forceinline__ double partner(double x) {
+  const long long b = __double_as_longlong(x);
+  const uint32_t lo = (uint32_t)partner<S>((int)(uint32_t)b);
+  const uint32_t hi = (uint32_t)partner<S>((int)(uint32_t)(b >> 32));
+  return __longlong_as_double((long long)(((unsigned long long)hi << 32) | lo));
+}
+template <int LANES, int S = 0>
+__device__ __forceinline__ float group_sum(float x) {
+  if constexpr ((1 << S) < LANES) return group_sum<LANES, S + 1>(x + partner<S>(x));
+  else return x;
+}
+template <int LANES, int S = 0>
 __device__ __forceinline__ float group_max(float x) {
+  if constexpr ((1 << S) < LANES) return group_max<LANES, S + 1>(fmaxf(x, partner<S>(x)));
+  else return x;
+}
+template <int LANES, int S = 0>
+__device__ __forceinline__ uint32_t group_max(uint32_t x) {
+  if constexpr ((1 << S) < LANES) return group_max<LANES, S + 1>(max(x, (uint32_t)partner<S>((int)x)));
+  else return x;
+}
+template <int LANES, int S = 0>
+__device__ __forceinline__ uint32_t group_min(uint32_t x) {
+  if constexpr ((1 << S) < LANES) return group_min<LANES, S + 1>(min(x, (uint32_t)partner<S>((int)x)));
+  else return x;
+}
+// The largest key of all lanes, of equal ones the lower expert's.
+template <int LANES, int S = 0>
+__device__ __forceinline__ void group_best(double& best, int& at) {
+  if constexpr ((1 << S) < LANES) {
+    const double ob = partner<S>(best);
+    const int oa = partner<S>(at);
+    if (ob > best || (ob == best && oa < at)) {
+      best = ob;
+      at = oa;
+    }
+    group_best<LANES, S + 1>(best, at);
+  }
+}
+
+// sigmoid with expf and the exact division: the weights' own accuracy
+__device__ __forceinline__ float sigmoid_exact(float x) { return 1.f / (1.f + expf(-x)); }
+
+// A float32 key as a whole number of the same order; 0 is no key (-inf).
+__device__ __forceinline__ uint32_t ordered(float key) {
+  if (!(key > kNegInf)) return 0u;
+  const uint32_t b = __float_as_uint(key + 0.f);   // -0 counts as 0
+  return b >> 31 ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t o) {
+  return __uint_as_float(o >> 31 ? o & 0x7FFFFFFFu : ~o);
+}
+
+// The experts of the K largest keys of the group's row, lane k holding slot
+// k's (-1 where nothing is left).  Spends the keys.  A round finds the largest
+// key of all lanes first and then the lowest expert that has it: two chains of
+// one-instruction steps, half the work of carrying both through one.  CHECK:
+// keys that are only nearly exact.  Rounds go on past K while a key is within
+// 2^-19 (1 + the larger magnitude) of the one before it, or not ordered with
+// it; `close` tells whether there were such neighbours at all, and `found` how
+// many experts the lanes hold (LANES: perhaps not all that are near).
+template <int LANES, int V, bool CHECK>
+__device__ __forceinline__ int select(uint32_t (&key)[V], int l, int K, bool& close, int& found) {
+  int mine = -1;   // lane k keeps the expert of round k
+  float before = 0.f;
+  const int first = expert_of<LANES, V>(l, 0);
+  close = false;
+  int k = 0;
+  for (; k < (CHECK ? LANES : K); ++k) {
+    uint32_t best = key[0];
 #pragma unroll
-  for (int m = 1; m < LANES; m <<= 1) x = fmaxf(x, __shfl_xor(x, m, LANES));
-  return x;
+    for (int v = 1; v < V; ++v) best = max(best, key[v]);
+    best = group_max<LANES>(best);
+    if (best == 0u) break;   // the whole group agrees; later slots keep -1
+    if (CHECK) {
+      const float now = unordered(best);
+      const bool clear = before - now > 0x1p-19f * (1.f + fmaxf(fabsf(before), fabsf(now)));
+      if (k >= K && clear) break;
+      close |= k > 0 && !clear;
+      before = now;
+    }
+    uint32_t at = 0x7FFFFFFFu;
+#pragma unroll
+    for (int v = V - 1; v >= 0; --v)   // experts ascend with v
+      if (key[v] == best) at = expert_of<LANES, V>(0, v);
+    at = group_min<LANES>(at + first);
+    if (l == k) mine = (int)at;
+    at -= first;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (at == (uint32_t)expert_of<LANES, V>(0, v)) key[v] = 0u;
+  }
+  found = k;
+  return mine;
+}
+
+// The lanes' experts in the order of their float64 keys, equal ones by expert:
+// lane r gets the one with r others before it.  Lanes without an expert (-1)
+// are last.
+template <int LANES>
+__device__ __forceinline__ int reorder(double key, int mine, int l, int found) {
+  int rank = 0;
+  for (int j = 0; j < found; ++j) {
+    const double kj = __shfl(key, j, LANES);
+    const int ej = __shfl(mine, j, LANES);
+    rank += kj > key || (kj == key && ej < mine);
+  }
+  if (mine < 0) rank = LANES;
+  int out = -1;
+  for (int j = 0; j < found; ++j) {
+    const int rj = __shfl(rank, j, LANES), ej = __shfl(mine, j, LANES);
+    if (rj == l) out = ej;
+  }
+  return out;
+}
+
+// The selection key in float64.
+__device__ __forceinline__ double exact_key(float x, float bias) {
+  return 1.0 / (1.0 + exp(-(double)x)) + (double)bias;
+}
+
+// select() from float64 keys.
+template <int LANES, int V>
+__device__ __forceinline__ int select_exact(double (&key)[V], int l, int K) {
+  int mine = -1;
+  for (int k = 0; k < K; ++k) {
+    double best = key[0];
+    int at = expert_of<LANES, V>(l, 0);
+#pragma unroll
+    for (int v = 1; v < V; ++v)   // experts ascend with v: the first of equals stays
+      if (key[v] > best) {
+        best = key[v];
+        at = expert_of<LANES, V>(l, v);
+      }
+    group_best<LANES>(best, at);
+    if (!(best > -__builtin_inf())) break;
+    if (l == k) mine = at;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (expert_of<LANES, V>(l, v) == at) key[v] = -__builtin_inf();
+  }
+  return mine;
 }
 
 __device__ __forceinline__ float ratio(float num, float den) { return den > 0.f ? num / den : 0.f; }
 
-template <typename T, typename Key, int LANES, int V, bool SIGMOID>
+template <typename T, int LANES, int V, bool SIGMOID, bool BIASED>
 __global__ __launch_bounds__(kThreads) void gate_kernel(
     const T* __restrict__ logits, const float* __restrict__ bias, int64_t rows, int E, int K,
     bool renorm, float scale, int32_t* __restrict__ ids, float* __restrict__ weights) {
@@ -128,43 +279,40 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(
       for (int v = 0; v < V; ++v) all += expf(x[v] - top);
       all = group_sum<LANES>(all);
     }
-    Key key[V];
+    uint32_t key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if constexpr (sizeof(Key) == 8) {
-        const int e = expert_of<LANES, V>(l, v);
-        const double k = 1.0 / (1.0 + exp(-(double)x[v])) + (e < E ? (double)bias[e] : 0.0);
-        key[v] = x[v] > kNegInf && k == k ? k : -__builtin_inf();
+      const int e = expert_of<LANES, V>(l, v);
+      float k = x[v];
+      if constexpr (BIASED) {
+        k = sigmoid_f32(x[v]) + (e < E ? bias[e] : 0.f);
+        if (!(x[v] > kNegInf && k == k)) k = kNegInf;
+      }
+      key[v] = ordered(k);
+    }
+    bool close;
+    int found;
+    int mine = select<LANES, V, BIASED>(key, l, K, close, found);
+    if (BIASED && close) {
+      // float32 keys are within 2^-21 (1 + |key|) of the float64 ones (sigmoid
+      // to 2^-22, the sum's rounding 2^-24 |key|): neighbours further apart
+      // than that are in float64's order.  This row has some that are not.
+      if (found < LANES) {   // all that matter are here, one a lane
+        double k = -__builtin_inf();
+        if (mine >= 0) k = exact_key(logit(row, mine), bias[mine]);
+        mine = reorder<LANES>(k, mine, l, found);
       } else {
-        key[v] = x[v];
+        double all_keys[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int e = expert_of<LANES, V>(l, v);
+          const double k = exact_key(x[v], e < E ? bias[e] : 0.f);
+          all_keys[v] = x[v] > kNegInf && k == k ? k : -__builtin_inf();
+        }
+        mine = select_exact<LANES, V>(all_keys, l, K);
       }
     }
-    int mine = -1;   // lane k keeps the expert of slot k
-    for (int k = 0; k < K; ++k) {
-      Key best = key[0];
-      int at = expert_of<LANES, V>(l, 0);
-#pragma unroll
-      for (int v = 1; v < V; ++v)   // experts ascend with v: the first of equals stays
-        if (key[v] > best) {
-          best = key[v];
-          at = expert_of<LANES, V>(l, v);
-        }
-#pragma unroll
-      for (int m = 1; m < LANES; m <<= 1) {
-        const Key ob = __shfl_xor(best, m, LANES);
-        const int oa = __shfl_xor(at, m, LANES);
-        if (ob > best || (ob == best && oa < at)) {
-          best = ob;
-          at = oa;
-        }
-      }
-      const bool some = best > (Key)kNegInf;
-      if (l == k) mine = some ? at : -1;
-      if (!some) break;   // the whole group agrees; later slots keep -1
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (expert_of<LANES, V>(l, v) == at) key[v] = (Key)kNegInf;
-    }
+    if (BIASED && l >= K) mine = -1;   // near ones past the last slot
     const float v = mine >= 0 ? logit(row, mine) : kNegInf;
     float w;
     if (!SIGMOID) {
@@ -173,7 +321,7 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(
       w = ratio(w, renorm ? group_sum<LANES>(w) : all);
     } else {
       const float m = fmaxf(group_max<LANES>(v), -kMaxF32);
-      w = mine < 0 ? 0.f : renorm && m < -30.f ? expf(v - m) : sigmoid_f32(v);
+      w = mine < 0 ? 0.f : renorm && m < -30.f ? expf(v - m) : sigmoid_exact(v);
       if (renorm) w = ratio(w, group_sum<LANES>(w));
     }
     if (l < K) {
@@ -231,8 +379,8 @@ __global__ __launch_bounds__(kThreads) void gate_backward_kernel(
         const float p = ratio(e, group_sum<LANES>(e));
         d = scale * p * (d - group_sum<LANES>(p * d));
       } else {
-        const float sg = v > kNegInf ? sigmoid_f32(v) : 0.f;
-        const float co = v > kNegInf ? sigmoid_f32(-v) : 0.f;
+        const float sg = v > kNegInf ? sigmoid_exact(v) : 0.f;
+        const float co = v > kNegInf ? sigmoid_exact(-v) : 0.f;
         if (renorm) {
           const float e = m < -30.f ? expf(v - m) : sg;
           const float r = ratio(e, group_sum<LANES>(e));
@@ -307,13 +455,13 @@ hipError_t gate(int score, bool renorm, float scale, const T* logits, const floa
     constexpr int lanes = decltype(L)::value, vals = decltype(V)::value;
     const dim3 grid(blocks_for(rows, lanes)), block(kThreads);
     if (score == LRMOE_GATE_SOFTMAX)
-      hipLaunchKernelGGL((gate_kernel<T, float, lanes, vals, false>), grid, block, 0, s, logits,
+      hipLaunchKernelGGL((gate_kernel<T, lanes, vals, false, false>), grid, block, 0, s, logits,
                          bias, rows, E, K, renorm, scale, ids, w);
     else if (bias == nullptr)
-      hipLaunchKernelGGL((gate_kernel<T, float, lanes, vals, true>), grid, block, 0, s, logits,
+      hipLaunchKernelGGL((gate_kernel<T, lanes, vals, true, false>), grid, block, 0, s, logits,
                          bias, rows, E, K, renorm, scale, ids, w);
     else
-      hipLaunchKernelGGL((gate_kernel<T, double, lanes, vals, true>), grid, block, 0, s, logits,
+      hipLaunchKernelGGL((gate_kernel<T, lanes, vals, true, true>), grid, block, 0, s, logits,
                          bias, rows, E, K, renorm, scale, ids, w);
   });
   return hipGetLastError();

@@ -32,7 +32,8 @@ namespace {
 // (a decoding step); more take a histogram launch first.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kOneBlock = 8192;
+constexpr int kOneBlock = 4096;   // ids of a call that one workgroup sorts
+constexpr int kBlockIds = 2048;   // ids of a workgroup otherwise
 constexpr int kMaxBlocks = 1024;
 constexpr int kMaxBins = kMaxSegs + 1;
 
@@ -43,7 +44,7 @@ struct SortShape {
 };
 SortShape sort_shape(int64_t n) {
   SortShape s;
-  int64_t blocks = n <= kOneBlock ? 1 : (n + kOneBlock - 1) / kOneBlock;
+  int64_t blocks = n <= kOneBlock ? 1 : (n + kBlockIds - 1) / kBlockIds;
   if (blocks > kMaxBlocks) blocks = kMaxBlocks;
   const int64_t per = (n + blocks - 1) / blocks;
   s.per_wave = (per + kSortThreads - 1) / kSortThreads * 64;
@@ -56,6 +57,18 @@ SortShape sort_shape(int64_t n) {
 
 __device__ __forceinline__ int bin_of(int id, int E) { return id >= 0 && id < E ? id : E; }
 
+// Counts ids[i] of the wave's live lanes.  Bin E, which holds most pairs where
+// most experts are on other ranks, is counted by a ballot: atomics of many
+// lanes on one address go one after the other.
+__device__ __forceinline__ void count(uint32_t* h, const int32_t* ids, int64_t i, int64_t hi,
+                                      int E) {
+  const bool live = i < hi;
+  const int e = live ? bin_of(ids[i], E) : E;
+  const unsigned long long others = __ballot(live && e == E);
+  if (e < E) atomicAdd(&h[e], 1u);
+  if ((threadIdx.x & 63) == 0 && others) atomicAdd(&h[E], (uint32_t)__popcll(others));
+}
+
 __global__ __launch_bounds__(kSortThreads) void sort_hist_kernel(const int32_t* __restrict__ ids,
                                                                  int64_t n, int E,
                                                                  int64_t per_block,
@@ -66,7 +79,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_hist_kernel(const int32_t* 
   __syncthreads();
   const int64_t lo = blockIdx.x * per_block;
   const int64_t hi = lo + per_block < n ? lo + per_block : n;
-  for (int64_t i = lo + tid; i < hi; i += kSortThreads) atomicAdd(&h[bin_of(ids[i], E)], 1u);
+  for (int64_t i0 = lo + (tid & ~63); i0 < hi; i0 += kSortThreads) count(h, ids, i0 + (tid & 63), hi, E);
   __syncthreads();
   for (int e = tid; e <= E; e += kSortThreads) hist[(int64_t)blockIdx.x * (E + 1) + e] = h[e];
 }
@@ -86,11 +99,12 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(
   __syncthreads();
   const int64_t lo = blockIdx.x * per_block + wave * per_wave;
   const int64_t hi = lo + per_wave < n ? lo + per_wave : n;
-  for (int64_t i = lo + lane; i < hi; i += 64) atomicAdd(&wave_h[wave][bin_of(ids[i], E)], 1u);
+  for (int64_t i0 = lo; i0 < hi; i0 += 64) count(wave_h[wave], ids, i0 + lane, hi, E);
   if (blocks > 1) {
     // 4 groups of 256 threads add up every fourth workgroup's histogram
     for (int e = tid & 255; e < bins; e += 256) {
       uint32_t all = 0, early = 0;
+#pragma unroll 8
       for (int b = tid >> 8; b < blocks; b += kSortThreads / 256) {
         const uint32_t c = hist[(int64_t)b * bins + e];
         all += c;

@@ -644,16 +644,16 @@ def pruned_backward(plan: Plan, alpha, g, phi, W, g_row_index=None, out=None, ws
 # current stream.
 
 def _arg(name: str, t: torch.Tensor, dtype, shape, dev):
-    """Device address of an argument, after checking it."""
+    """Device address of an argument, after checking it (None if it is empty)."""
+    if t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr() or None
     if t.dtype != dtype:
         raise TypeError(f"{name}: {dtype} expected, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {shape} expected, got {tuple(t.shape)}")
     if t.device != dev:
         raise ValueError(f"{name}: on {t.device}, the other tensors are on {dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: liblrmoe takes contiguous tensors")
-    return t.data_ptr() if t.numel() > 0 else None
+    raise ValueError(f"{name}: liblrmoe takes contiguous tensors")
 
 
 def _device(t: torch.Tensor):
@@ -662,15 +662,21 @@ def _device(t: torch.Tensor):
     return t.device
 
 
+# The current stream's handle without a Stream object around it (2 us a call).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _call(fn: str, dev, *args) -> None:
     """Run an entry point on `dev` (its last argument, the stream, is added)."""
-    f = getattr(lib(), fn)
-    if dev.index == torch.cuda.current_device():
-        st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    f = getattr(_lib_handle or lib(), fn)
+    at = dev.index
+    if at == torch.cuda.current_device():
+        st = f(*args, _raw_stream(at))
     else:
         with torch.cuda.device(dev):
-            st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
-    check(fn, st)
+            st = f(*args, _raw_stream(at))
+    if st != 0:
+        check(fn, st)
 
 
 def _workspace(need: int, ws: Optional[torch.Tensor], dev):

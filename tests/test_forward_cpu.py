@@ -72,13 +72,13 @@ def test_route_sort_refuses_and_sizes():
     for name in ("ids", "counts", "seg", "row", "pos"):
         assert call(**{name: None}) == NULL
         assert call(**{name: FAKE + 4}) == ALIGN
-    # 8192 slots and fewer need no workspace; more, one row of E + 1 counts a workgroup
-    assert L.route_sort_workspace_bytes(1024, 8, 16) == 0
-    n = L.route_sort_workspace_bytes(1025, 8, 16)
-    assert n == 2 * 17 * 4
-    assert call(T=1025, K=8, E=16, ws=None, n=n) == NULL
-    assert call(T=1025, K=8, E=16, ws=FAKE, n=n - 1) == WORKSPACE
-    assert call(T=1025, K=8, E=16, ws=FAKE + 4, n=n) == ALIGN
+    # 4096 slots and fewer need no workspace; more, one row of E + 1 counts a workgroup
+    assert L.route_sort_workspace_bytes(512, 8, 16) == 0
+    n = L.route_sort_workspace_bytes(513, 8, 16)
+    assert n == 3 * 17 * 4
+    assert call(T=513, K=8, E=16, ws=None, n=n) == NULL
+    assert call(T=513, K=8, E=16, ws=FAKE, n=n - 1) == WORKSPACE
+    assert call(T=513, K=8, E=16, ws=FAKE + 4, n=n) == ALIGN
     with pytest.raises(L.LrmoeError):
         L.route_sort_workspace_bytes(4, 2, 0)
 

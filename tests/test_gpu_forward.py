@@ -110,6 +110,36 @@ def test_gate_ties_masks_and_extremes(dt, score, biased):
                + HALF[dt] * want.abs(), "dlogits")
 
 
+@pytest.mark.parametrize("E,K", [(128, 8), (40, 3), (256, 16), (300, 20)])
+def test_gate_near_keys(E, K):
+    """Biased keys that float32 cannot order: differences of 2^-30 and less,
+    equal keys, whole rows of them (more than the lanes hold), keys at the
+    border of the K chosen, infinite biases."""
+    g = gen(E)
+    T = 12
+    x = normal(g, (T, E), F32, 1.0)
+    bias = normal(g, (E,), F32, 0.1)
+    key = torch.sigmoid(x.double())
+    # rows 0..5: x chosen so that the key of expert e is the row's common value
+    # to within float32's rounding of x
+    goal = 0.5 + 0.2 * torch.rand((6, 1), generator=g).double()
+    want = (goal - bias.double()).clamp(0.05, 0.95)
+    x[:6] = torch.log(want / (1 - want)).float()
+    x[3:6, K + 2:] = -3.0            # only a few near ones
+    x[6] = 0.25                      # equal logits, keys by bias alone
+    x[7, ::3] = float("-inf")
+    ids, w = O.gate(x, K, "sigmoid", bias, True, 1.0)
+    out = L.gate_topk(x.to(DEV), K, score=L.GATE_SIGMOID, select_bias=bias.to(DEV))
+    assert torch.equal(out["ids"].cpu().long(), ids)
+    within(out["weights"], w, gate_bound(x, w), "weights")
+    bias[:] = 0.125                  # equal biases: ties of equal logits
+    x[:, 1::2] = x[:, ::2][:, :x[:, 1::2].shape[1]]
+    bias[5], bias[6], bias[7] = float("inf"), float("-inf"), float("nan")
+    ids, w = O.gate(x, K, "sigmoid", bias, True, 1.0)
+    out = L.gate_topk(x.to(DEV), K, score=L.GATE_SIGMOID, select_bias=bias.to(DEV))
+    assert torch.equal(out["ids"].cpu().long(), ids)
+
+
 @pytest.mark.parametrize("T,E,K", GATE)
 @pytest.mark.parametrize("dt", [F32, BF16])
 @pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False),
