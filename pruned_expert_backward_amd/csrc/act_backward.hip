@@ -37,38 +37,32 @@ __device__ __forceinline__ void segment(const int32_t* seg, int e, int64_t P, in
 // Expert of run r and the run's number inside it, or false past the last run.
 // Every wave finds it for itself: lane l looks at experts 4 l .. 4 l + 3.
 __device__ __forceinline__ bool find_run(const int32_t* seg, int E, int64_t P, int64_t r, int& e,
-                                         int64_t& sub) {
+                                         int& sub) {
   const int lane = threadIdx.x & 63;
-  int64_t n[4], sum = 0;
+  int n[4], sum = 0;   // fewer than 2^31 / kRows + E runs in all
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     n[j] = 0;
     if (4 * lane + j < E) {
       int64_t lo, hi;
       segment(seg, 4 * lane + j, P, lo, hi);
-      n[j] = runs_of(hi - lo);
+      n[j] = (int)runs_of(hi - lo);
     }
     sum += n[j];
   }
-  int64_t end = sum;
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const int64_t o = __shfl_up(end, m, 64);
-    if (lane >= m) end += o;
-  }
+  const int end = wave_scan(sum);
   const unsigned long long past = __ballot(end > r);
   if (past == 0) return false;
   const int owner = __ffsll(past) - 1;
-  int64_t at = r - (end - sum);   // meant for the owner lane
-  int j = 0;
+  int at = (int)r - (end - sum), j = 0;   // meant for the owner lane
 #pragma unroll
   for (int i = 0; i < 3; ++i)
     if (j == i && at >= n[i]) {
       at -= n[i];
       j = i + 1;
     }
-  e = __builtin_amdgcn_readfirstlane(__shfl(4 * lane + j, owner, 64));
-  sub = __shfl(at, owner, 64);
+  e = __builtin_amdgcn_readlane(4 * lane + j, owner);
+  sub = __builtin_amdgcn_readlane(at, owner);
   return true;
 }
 
@@ -97,11 +91,12 @@ __global__ __launch_bounds__(kThreads) void act_backward_kernel(
   const int64_t run = blockIdx.x / pieces;
   const int col = (int)(blockIdx.x % pieces) * (LPR * N) + lane * N;
   int e;
-  int64_t sub;
+  int sub;
   if (!find_run(seg, E, P, run, e, sub)) return;   // the same answer in every wave
   int64_t lo, hi;
   segment(seg, e, P, lo, hi);
-  lo += sub * kRows;
+  if (sub < 0 || sub >= runs_of(hi - lo)) return;   // offsets out of order: counts overflowed
+  lo += (int64_t)sub * kRows;
   if (hi > lo + kRows) hi = lo + kRows;
   float acc[H][N];
 #pragma unroll

@@ -67,6 +67,18 @@ __device__ __forceinline__ void store_vals(T* p, const float (&v)[N]) {
   }
 }
 
+// Sum over lanes 0 .. this one, by DPP: inside rows of 16 lanes, then the last
+// lane of a row into the next one, of two rows into the next two.
+__device__ __forceinline__ int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);   // row_shr:1
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);   // row_bcast:15
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);   // row_bcast:31
+  return x;
+}
+
 // ---- activations, float32
 // Sigmoid from the hardware exp2 and reciprocal (about one ulp each; the
 // rounded argument adds |x| 2^-24 relative to exp(-x), which is at most 2^-25

@@ -29,13 +29,23 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 __device__ const vec4u zero_page[16] = {};
 
-__device__ __forceinline__ float activate(int act, float x) {
+// One (uniform) branch for N values.
+template <int N>
+__device__ __forceinline__ void activate(int act, float (&v)[N]) {
   switch (act) {
-    case LRMOE_ACT_RELU: return fmaxf(x, 0.f);
-    case LRMOE_ACT_SILU: return x * sigmoid_f32(x);
-    case LRMOE_ACT_GELU: return gelu_f32(x);
+    case LRMOE_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];   // NaN stays
+      break;
+    case LRMOE_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] *= sigmoid_f32(v[i]);
+      break;
+    case LRMOE_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = gelu_f32(v[i]);
+      break;
   }
-  return x;
 }
 
 // ---------------------------------------------------------------- tiles
@@ -70,12 +80,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* seg, int E, int64_t P, 
     n[j] = off[j + 1] > off[j] ? (int)((off[j + 1] - off[j] + tm - 1) / tm) : 0;
     sum += n[j];
   }
-  int end = sum;
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const int o = __shfl_up(end, m, 64);
-    if (lane >= m) end += o;
-  }
+  const int end = wave_scan(sum);
   const int all = __builtin_amdgcn_readlane(end, 63);
   const int64_t total = (int64_t)all * cols;
   const int64_t share = (total + 7) / 8;
@@ -88,8 +93,11 @@ __device__ __forceinline__ bool find_tile(const int32_t* seg, int E, int64_t P, 
   const int gr = left < kGroup ? left : kGroup;
   const int r = __builtin_amdgcn_readfirstlane(g * kGroup + in % gr);
   at.col = __builtin_amdgcn_readfirstlane(in / gr);
-  const int owner = __ffsll((unsigned long long)__ballot(end > r)) - 1;
+  const unsigned long long past = __ballot(end > r);
+  if (past == 0) return false;
+  const int owner = __ffsll(past) - 1;
   int sub = r - (end - sum), j = 0;   // meant for the owner lane
+  const bool sane = sub >= 0;         // offsets out of order may overflow the counts
 #pragma unroll
   for (int i = 0; i < 3; ++i)
     if (j == i && sub >= n[i]) {
@@ -99,12 +107,12 @@ __device__ __forceinline__ bool find_tile(const int32_t* seg, int E, int64_t P, 
   const int64_t lo = (j == 0 ? off[0] : j == 1 ? off[1] : j == 2 ? off[2] : off[3]) +
                      (int64_t)sub * tm;
   const int64_t hi = j == 0 ? off[1] : j == 1 ? off[2] : j == 2 ? off[3] : off[4];
-  const int rows = (int)(hi - lo < tm ? hi - lo : tm);
+  const int rows = sane ? (int)(hi - lo < tm ? hi - lo : tm) : 0;
   at.e = __builtin_amdgcn_readlane(4 * lane + j, owner);
   const uint32_t lo32 = __builtin_amdgcn_readlane((uint32_t)lo, owner);   // P < 2^31
   at.lo = lo32;
   at.rows = __builtin_amdgcn_readlane(rows, owner);
-  return true;
+  return at.rows > 0;
 }
 
 // Row of x of pair row u: null when its index is out of range (a zero row).
@@ -213,7 +221,7 @@ struct Gemm {
   // Chunk c of row r sits at slot c ^ swz(r): 16 consecutive rows of one chunk
   // (one LDS cycle of a 16-byte read) fall on 16 distinct bank groups.
   __device__ __forceinline__ static int swz(int r) {
-    return RB == 64 ? (r ^ (r >> 2)) & 3 : (r >> 1) & 7;
+    return RB == 64 ? (r ^ (r >> 2)) & 3 : RB == 128 ? (r >> 1) & 7 : r & 15;
   }
 
   const ForwardArgs& args;
@@ -227,7 +235,12 @@ struct Gemm {
   uint32_t off[FAR ? 1 : kLoads];
   const char* src[FAR ? kLoads : 1];
   int step[FAR ? kLoads : 1];
-  int chunk[2];            // byte offset of the lane's chunk inside the step, by block parity
+  // Byte offset of the lane's chunk inside the step, which depends on the LDS
+  // block of the load modulo kVar: a few values for each operand.
+  static constexpr int kRowsPer = 1024 / RB;   // rows of a load
+  static constexpr int kVar = RB == 64 ? 1 : 16 / kRowsPer;
+  static constexpr int kVarA = std::min(kPwA, kVar), kVarB = std::min(kPwB, kVar);
+  int cha[kVarA], chb[kVarB];
   uint32_t fa, fb;         // fragment base addresses (A rows, B rows of the wave)
   uint32_t fs[kSlices];    // lane's offset of each slice
 
@@ -254,17 +267,18 @@ struct Gemm {
       xbuf = buffer(x, rows * kbytes);
       wbuf = buffer(W, (int64_t)a.d_out * kbytes);
     }
-    constexpr int rows_per = 1024 / RB;
-    static_assert(kPwA % 2 == 0 || kWaves % 2 == 0 || RB == 64, "block parity");
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      chunk[j] = ((lane % kChunks) ^ swz(j * rows_per + lane / kChunks)) * 16;
+    for (int j = 0; j < kVarA; ++j)
+      cha[j] = ((lane % kChunks) ^ swz((wave * kPwA + j) * kRowsPer + lane / kChunks)) * 16;
+#pragma unroll
+    for (int j = 0; j < kVarB; ++j)
+      chb[j] = ((lane % kChunks) ^ swz((wave * kPwB + j) * kRowsPer + lane / kChunks)) * 16;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
       const bool isA = j < kPwA;
       const int blk = isA ? wave * kPwA + j : wave * kPwB + j - kPwA;
-      const int r = blk * rows_per + lane / kChunks;
-      const int ch = ((lane % kChunks) ^ swz(r)) * 16;
+      const int r = blk * kRowsPer + lane / kChunks;
+      const int ch = chunk_of(j);
       int64_t n;   // row of x or of the expert's weights
       bool ok;
       if (isA) {
@@ -299,6 +313,10 @@ struct Gemm {
     fb = lds + TM * RB + wn * WC * RB;
   }
 
+  __device__ __forceinline__ int chunk_of(int j) const {
+    return j < kPwA ? cha[j % kVarA] : chb[(j - kPwA) % kVarB];
+  }
+
   // Load j of K step kt into stage buffer `buf`.  Past the end of K it writes
   // zeros.
   __device__ __forceinline__ void issue(int j, int buf, int kt) {
@@ -309,10 +327,7 @@ struct Gemm {
     // uniform: the K step read (steps go round from k0), bytes left from there
     const int k = kt + k0 < nk ? kt + k0 : kt + k0 - nk;
     const int left = kt < nk ? kbytes - k * RB : 0;
-    // swz depends on the block's parity: known here where a wave has an even
-    // number of blocks, else from the wave
-    const int par = (isA ? kPwA : kPwB) % 2 == 0 ? (isA ? j : j - kPwA) & 1 : blk & 1;
-    const bool in = (RB == 64 ? chunk[0] : par ? chunk[1] : chunk[0]) < left;
+    const bool in = chunk_of(j) < left;
     if constexpr (FAR) {
       load_lds16(dst, in ? src[j] : reinterpret_cast<const char*>(zero_page));
       src[j] += step[j];
@@ -476,7 +491,8 @@ struct Gemm {
               for (int i = 0; i < UN; ++i) v[i] = z[i] * sigmoid_f32(z[i]) * w[i];
             } else {
 #pragma unroll
-              for (int i = 0; i < UN; ++i) v[i] = activate(args.act, z[i]);
+              for (int i = 0; i < UN; ++i) v[i] = z[i];
+              activate(args.act, v);
             }
             if (args.residual != nullptr) {
               float r8[UN];
@@ -530,10 +546,8 @@ __device__ __forceinline__ bool find_ragged_tile(const int32_t* seg, int E, int6
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (off[j + 1] > off[j]) halves += (int)((off[j + 1] - off[j] + 127) / 128);
-#pragma unroll
-  for (int m = 32; m > 0; m >>= 1) halves += __shfl_xor(halves, m, 64);
-  const int tm =
-      (int64_t)__builtin_amdgcn_readfirstlane(halves) * cols <= kXcds * kXcdCus ? 128 : 256;
+  halves = __builtin_amdgcn_readlane(wave_scan(halves), 63);
+  const int tm = (int64_t)halves * cols <= kXcds * kXcdCus ? 128 : 256;
   int n[4], full = 0, part = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -541,15 +555,8 @@ __device__ __forceinline__ bool find_ragged_tile(const int32_t* seg, int E, int6
     full += n[j] / tm;
     part += n[j] % tm != 0;
   }
-  int fend = full, pend = part;   // whole tiles and ends up to this lane's experts
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const int f = __shfl_up(fend, m, 64), q = __shfl_up(pend, m, 64);
-    if (lane >= m) {
-      fend += f;
-      pend += q;
-    }
-  }
+  // whole tiles and ends up to this lane's experts
+  const int fend = wave_scan(full), pend = wave_scan(part);
   const int fulls = __builtin_amdgcn_readlane(fend, 63);
   const int parts = __builtin_amdgcn_readlane(pend, 63);
   const int x = blockIdx.x % kXcds;
@@ -583,9 +590,11 @@ __device__ __forceinline__ bool find_ragged_tile(const int32_t* seg, int E, int6
   }
   r = __builtin_amdgcn_readfirstlane(r);
   at.col = __builtin_amdgcn_readfirstlane(at.col);
-  const int owner =
-      __ffsll((unsigned long long)(whole ? __ballot(fend > r) : __ballot(pend > r))) - 1;
+  const unsigned long long past = whole ? __ballot(fend > r) : __ballot(pend > r);
+  if (past == 0) return false;
+  const int owner = __ffsll(past) - 1;
   int sub = whole ? r - (fend - full) : r - (pend - part), j = 0;   // meant for the owner lane
+  const bool sane = sub >= 0;
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
     const int c = whole ? n[i] / tm : (int)(n[i] % tm != 0);
@@ -599,6 +608,7 @@ __device__ __forceinline__ bool find_ragged_tile(const int32_t* seg, int E, int6
   const int first = (whole ? sub : nj / tm) * tm + piece * (tm / cut);
   int rows = nj - first;
   if (rows > tm / cut) rows = tm / cut;
+  if (!sane) rows = 0;
   at.e = __builtin_amdgcn_readlane(4 * lane + j, owner);
   at.lo = (uint32_t)__builtin_amdgcn_readlane((uint32_t)(oj + first), owner);   // P < 2^31
   at.rows = __builtin_amdgcn_readlane(rows, owner);
@@ -616,7 +626,7 @@ __device__ __forceinline__ void run_tile(const ForwardArgs& args, const TileAt& 
 
 template <typename T, bool GLU>
 struct Ragged {
-  typedef Gemm<T, 16, 128, 64, 2, 4, 128, 2, GLU> G256;
+  typedef Gemm<T, 16, 64, 128, 4, 2, 128, 2, GLU> G256;
   typedef Gemm<T, 16, 64, 64, 2, 4, 128, 3, GLU> G128;
   typedef Gemm<T, 16, 32, 64, 2, 4, 128, 3, GLU> G64;
   static constexpr int kLds = std::max(std::max(G256::kLds, G128::kLds), G64::kLds);
@@ -744,7 +754,9 @@ __global__ __launch_bounds__(256) void few_rows_kernel(ForwardArgs args, int col
       if (args.pre_b != nullptr) put(args.pre_b, o, b);
       v = z * sigmoid_f32(z) * b;
     } else {
-      v = activate(args.act, z);
+      float one[1] = {z};
+      activate(args.act, one);
+      v = one[0];
     }
     if (args.residual != nullptr) v += get(args.residual, o);
     put(y, o, v);
