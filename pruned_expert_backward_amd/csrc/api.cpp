@@ -8,12 +8,32 @@
 #include <numeric>
 #include <vector>
 
-#include "checks.h"
 #include "lrmoe_internal.h"
 
 using namespace lrmoe;
 
 namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Pointer rules: a NULL pointer is accepted only for an empty array.
+lrmoe_status need(const void* p, int64_t elems) {
+  if (elems == 0) return LRMOE_OK;
+  if (p == nullptr) return LRMOE_ERR_NULL;
+  if (!aligned16(p)) return LRMOE_ERR_ALIGN;
+  return LRMOE_OK;
+}
+
+lrmoe_status optional(const void* p) {
+  if (p != nullptr && !aligned16(p)) return LRMOE_ERR_ALIGN;
+  return LRMOE_OK;
+}
+
+#define LRMOE_TRY(x)                      \
+  do {                                    \
+    lrmoe_status _s = (x);                \
+    if (_s != LRMOE_OK) return _s;        \
+  } while (0)
 
 struct Checked {
   int64_t M = 0;
@@ -235,6 +255,8 @@ void group_shape(int nt, int pref, int32_t& gm, int32_t& gn) {
   gn = best;
   gm = kGroupSlots / best;
 }
+
+lrmoe_status hip_status(hipError_t e) { return e == hipSuccess ? LRMOE_OK : LRMOE_ERR_HIP; }
 
 // ---- Selection scratch for callers that cannot allocate
 // (lrmoe_score_select_compact_noalloc).  A file-scope device array: every GPU

@@ -1,4 +1,4 @@
-// Argument checks shared by the entry points (all on the host, before any
+// Argument checks of the forward-side entry points (all on the host, before any
 // launch).
 #pragma once
 
