@@ -13,6 +13,8 @@
 // LPR lanes take a row each in turn and keep the column sums in registers,
 // which meet in LDS and go to the workspace, one row of sums for each run.  A second kernel
 // adds an expert's runs in order, so the sums do not depend on timing.
+#include <algorithm>
+
 #include "forward.h"
 
 namespace lrmoe {
@@ -82,84 +84,86 @@ template <typename T, typename TO, int N, int ACT, int LPR>
 __global__ __launch_bounds__(kThreads) void act_backward_kernel(
     const int32_t* __restrict__ seg, const T* __restrict__ dy, const T* __restrict__ pa,
     const T* __restrict__ pb, int64_t P, int E, int F, TO* __restrict__ dz,
-    float* __restrict__ sums, int pieces) {
+    float* __restrict__ sums, int64_t runs) {
   constexpr bool GLU = ACT == LRMOE_ACT_SWIGLU;
   constexpr int H = GLU ? 2 : 1;
   constexpr int kGroups = kThreads / LPR;   // rows at a time
   __shared__ float part[kGroups - 1][H * N][LPR];
   const int tid = threadIdx.x, lane = tid % LPR, group = tid / LPR;
-  const int64_t run = blockIdx.x / pieces;
-  const int col = (int)(blockIdx.x % pieces) * (LPR * N) + lane * N;
-  int e;
-  int sub;
-  if (!find_run(seg, E, P, run, e, sub)) return;   // the same answer in every wave
-  int64_t lo, hi;
-  segment(seg, e, P, lo, hi);
-  if (sub < 0 || sub >= runs_of(hi - lo)) return;   // offsets out of order: counts overflowed
-  lo += (int64_t)sub * kRows;
-  if (hi > lo + kRows) hi = lo + kRows;
-  float acc[H][N];
-#pragma unroll
-  for (int h = 0; h < H; ++h)
-#pragma unroll
-    for (int i = 0; i < N; ++i) acc[h][i] = 0.f;
-  if (col < F) {
-    // kBatch rows in flight: their loads go out before the first is used
-    for (int64_t u0 = lo + group; u0 < hi; u0 += kBatch * kGroups) {
-      float g[kBatch][N], a[kBatch][N], b[kBatch][N];
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int64_t u = u0 + k * kGroups;
-        if (u < hi) {
-          load_vals(dy + u * F + col, g[k]);
-          if (ACT != LRMOE_ACT_NONE) load_vals(pa + u * F + col, a[k]);
-          if (GLU) load_vals(pb + u * F + col, b[k]);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int64_t u = u0 + k * kGroups;
-        if (u >= hi) break;
-        float z[H][N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          if constexpr (GLU) {
-            const float s = sigmoid_f32(a[k][i]), as = a[k][i] * s;
-            z[0][i] = g[k][i] * b[k][i] * (s + as * (1.f - s));
-            z[H - 1][i] = g[k][i] * as;
-          } else if constexpr (ACT == LRMOE_ACT_RELU) {
-            z[0][i] = a[k][i] > 0.f ? g[k][i] : 0.f;
-          } else if constexpr (ACT == LRMOE_ACT_NONE) {
-            z[0][i] = g[k][i];
-          } else {
-            z[0][i] = g[k][i] * act_grad<ACT>(a[k][i]);
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          store_vals(dz + (u * H + h) * F + col, z[h]);
-#pragma unroll
-          for (int i = 0; i < N; ++i) acc[h][i] += z[h][i];
-        }
-      }
-    }
-  }
-  if (sums == nullptr) return;
-  if (group > 0)
+  const int col = (int)blockIdx.y * (LPR * N) + lane * N;
+  // runs go by the grid's stride: a launch holds fewer than 2^32 threads
+  for (int64_t run = blockIdx.x; run < runs; run += gridDim.x) {
+    int e, sub;
+    if (!find_run(seg, E, P, run, e, sub)) return;   // the same answer in every wave
+    int64_t lo, hi;
+    segment(seg, e, P, lo, hi);
+    if (sub < 0 || sub >= runs_of(hi - lo)) continue;   // offsets out of order: counts overflowed
+    lo += (int64_t)sub * kRows;
+    if (hi > lo + kRows) hi = lo + kRows;
+    float acc[H][N];
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
-      for (int i = 0; i < N; ++i) part[group - 1][h * N + i][lane] = acc[h][i];
-  __syncthreads();
-  if (group == 0 && col < F) {
+      for (int i = 0; i < N; ++i) acc[h][i] = 0.f;
+    if (col < F) {
+      // kBatch rows in flight: their loads go out before the first is used
+      for (int64_t u0 = lo + group; u0 < hi; u0 += kBatch * kGroups) {
+        float g[kBatch][N], a[kBatch][N], b[kBatch][N];
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
+        for (int k = 0; k < kBatch; ++k) {
+          const int64_t u = u0 + k * kGroups;
+          if (u < hi) {
+            load_vals(dy + u * F + col, g[k]);
+            if (ACT != LRMOE_ACT_NONE) load_vals(pa + u * F + col, a[k]);
+            if (GLU) load_vals(pb + u * F + col, b[k]);
+          }
+        }
 #pragma unroll
-      for (int i = 0; i < N; ++i)
+        for (int k = 0; k < kBatch; ++k) {
+          const int64_t u = u0 + k * kGroups;
+          if (u >= hi) break;
+          float z[H][N];
 #pragma unroll
-        for (int w = 0; w < kGroups - 1; ++w) acc[h][i] += part[w][h * N + i][lane];
-      store_vals(sums + (run * H + h) * F + col, acc[h]);
+          for (int i = 0; i < N; ++i) {
+            if constexpr (GLU) {
+              const float s = sigmoid_f32(a[k][i]), as = a[k][i] * s;
+              z[0][i] = g[k][i] * b[k][i] * (s + as * (1.f - s));
+              z[H - 1][i] = g[k][i] * as;
+            } else if constexpr (ACT == LRMOE_ACT_RELU) {
+              z[0][i] = a[k][i] > 0.f ? g[k][i] : 0.f;
+            } else if constexpr (ACT == LRMOE_ACT_NONE) {
+              z[0][i] = g[k][i];
+            } else {
+              z[0][i] = g[k][i] * act_grad<ACT>(a[k][i]);
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            store_vals(dz + (u * H + h) * F + col, z[h]);
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[h][i] += z[h][i];
+          }
+        }
+      }
     }
+    if (sums == nullptr) continue;
+    if (group > 0)
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int i = 0; i < N; ++i) part[group - 1][h * N + i][lane] = acc[h][i];
+    __syncthreads();
+    if (group == 0 && col < F) {
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int w = 0; w < kGroups - 1; ++w) acc[h][i] += part[w][h * N + i][lane];
+        store_vals(sums + (run * H + h) * F + col, acc[h]);
+      }
+    }
+    __syncthreads();   // the next run writes the same LDS
   }
 }
 
@@ -203,16 +207,15 @@ __global__ __launch_bounds__(64 * kSumWaves) void dbias_kernel(const int32_t* __
 template <typename T, typename TO, int N, int LPR>
 hipError_t run(int act, const int32_t* seg, const void* dy, const void* a, const void* b, int64_t P,
                int E, int F, void* dz, float* sums, hipStream_t s) {
-  const int pieces = (F + LPR * N - 1) / (LPR * N);
-  const int64_t blocks = max_runs(P, E) * pieces;
-  if (blocks == 0) return hipSuccess;
-  if (blocks >= int64_t(1) << 24) return hipErrorInvalidValue;   // 2^32 threads
-  const dim3 grid((uint32_t)blocks), block(kThreads);
+  const int64_t runs = max_runs(P, E);
+  if (runs == 0) return hipSuccess;
+  const dim3 grid((uint32_t)std::min<int64_t>(runs, 1 << 22), (F + LPR * N - 1) / (LPR * N));
+  const dim3 block(kThreads);
 #define LRMOE_ACT(A)                                                                               \
   case A:                                                                                          \
     hipLaunchKernelGGL((act_backward_kernel<T, TO, N, A, LPR>), grid, block, 0, s, seg,            \
                        static_cast<const T*>(dy), static_cast<const T*>(a),                        \
-                       static_cast<const T*>(b), P, E, F, static_cast<TO*>(dz), sums, pieces);     \
+                       static_cast<const T*>(b), P, E, F, static_cast<TO*>(dz), sums, runs);       \
     break
   switch (act) {
     LRMOE_ACT(LRMOE_ACT_NONE);

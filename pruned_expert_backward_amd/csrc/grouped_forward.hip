@@ -9,8 +9,8 @@
 //
 // Both operands are rows along K (x rows, W rows), so they move to LDS as they
 // are and fragments are 16-byte LDS reads; the same kernel serves bfloat16
-// (v_mfma_f32_32x32x16_bf16, 8 values a fragment) and float32
-// (v_mfma_f32_32x32x2_f32, 4 values a fragment, four products), float32
+// (v_mfma_f32_16x16x32_bf16, 8 values a fragment) and float32
+// (v_mfma_f32_16x16x4_f32, 4 values a fragment, four products), float32
 // accumulation in both.  Masked rows and the end of K read a page of zeros.
 #include <algorithm>
 #include <type_traits>
@@ -24,7 +24,6 @@ namespace {
 #define LDS_AS __attribute__((address_space(3)))
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 __device__ const vec4u zero_page[16] = {};
@@ -62,8 +61,8 @@ struct TileAt {
 
 // Tile of this workgroup, or false.  Workgroup b runs on XCD b % 8, so each
 // XCD takes a contiguous eighth of the tiles; inside it, kGroup row tiles go
-// column by column.  Each wave finds the tile for
-// itself: lane l counts the tiles of experts 4 l .. 4 l + 3.
+// column by column.  Each wave finds the tile for itself: lane l counts the
+// tiles of experts 4 l .. 4 l + 3.
 __device__ __forceinline__ bool find_tile(const int32_t* seg, int E, int64_t P, int tm, int cols,
                                           TileAt& at) {
   const int lane = threadIdx.x & 63;
@@ -123,24 +122,19 @@ __device__ __forceinline__ const char* x_row(const ForwardArgs& a, int64_t u) {
   return reinterpret_cast<const char*>(static_cast<const T*>(a.x) + r * a.d_in);
 }
 
-// Products of 16-byte fragments (MI x MI results): one bf16 product of 16
-// (MI = 32) or 32 (MI = 16) values of K, or four float32 products of 2 or 4
-// values.
-template <int MI>
-using Acc = typename std::conditional<MI == 32, f32x16, f32x4>::type;
-template <typename T, int MI>
-__device__ __forceinline__ Acc<MI> mfma(vec4u a, vec4u b, Acc<MI> c) {
+// 16 x 16 products of 16-byte fragments: one bf16 product of 32 values of K, or
+// four float32 products of 4 values.  (32 x 32 results, the same rate with half
+// the fragments, were 5 to 8 % slower here: twice the accumulator traffic.)
+template <typename T>
+__device__ __forceinline__ f32x4 mfma(vec4u a, vec4u b, f32x4 c) {
   if constexpr (sizeof(T) == 2) {
-    const bf16x8 x = __builtin_bit_cast(bf16x8, a), y = __builtin_bit_cast(bf16x8, b);
-    if constexpr (MI == 32) return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, c, 0, 0, 0);
-    else return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = __uint_as_float(a[i]), y = __uint_as_float(b[i]);
-      if constexpr (MI == 32) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x, y, c, 0, 0, 0);
-      else c = __builtin_amdgcn_mfma_f32_16x16x4f32(x, y, c, 0, 0, 0);
-    }
+    for (int i = 0; i < 4; ++i)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c, 0,
+                                               0, 0);
     return c;
   }
 }
@@ -193,22 +187,20 @@ __device__ __forceinline__ void wait_loads_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// T: storage.  MI: size of an MFMA result.  A wave computes WR x WC, WM x WN
-// waves a workgroup.  RB: bytes of one row in one K step (64 or 128).  NS:
-// LDS stages.
-template <typename T, int MI, int WR, int WC, int WM, int WN, int RB, int NS, bool GLU,
-          bool FAR = false>
+// T: storage.  A wave computes WR x WC, WM x WN waves a workgroup, NS LDS
+// stages of one K step (128 bytes of every row) each.
+template <typename T, int WR, int WC, int WM, int WN, int NS, bool GLU, bool FAR = false>
 struct Gemm {
-  static constexpr int kMI = MI, MB = WR / MI, NB = WC / MI;
+  static constexpr int MI = 16, RB = 128;                  // MFMA rows; row bytes of a K step
+  static constexpr int MB = WR / MI, NB = WC / MI;
   static constexpr int kMB = MB, kNB = NB;
   static constexpr int kWaves = WM * WN;
   static constexpr int kThreads = 64 * kWaves;
-  static constexpr int kWavesPerSimd = WR * WC > 8192 ? 1 : 2;
+  static constexpr int kWavesPerSimd = 2;
   static constexpr int TM = WM * WR, TN = WN * WC;
   static constexpr int kOut = GLU ? TN / 2 : TN;           // columns of y
-  static constexpr int kSliceBytes = MI == 32 ? 32 : 64;   // K bytes of one MFMA
+  static constexpr int kSliceBytes = 64;                   // K bytes of one MFMA
   static constexpr int kSlices = RB / kSliceBytes;         // MFMA steps of a K step
-  static constexpr int kUnroll = kSlices % 2 ? 2 : 1;      // K steps a round: fragment sets alternate
   static constexpr int kChunks = RB / 16;
   static constexpr int kStage = (TM + TN) * RB;
   static constexpr int kPwA = TM * RB / 1024 / kWaves, kPwB = TN * RB / 1024 / kWaves;
@@ -217,11 +209,12 @@ struct Gemm {
   static constexpr int kLds = NS * kStage > kEpi ? NS * kStage : kEpi;
   static_assert(TM * RB % (1024 * kWaves) == 0 && TN * RB % (1024 * kWaves) == 0, "whole loads");
   static_assert(!GLU || NB % 2 == 0, "gate and up blocks of a wave");
+  static_assert(kSlices % 2 == 0, "fragment sets alternate");
 
   // Chunk c of row r sits at slot c ^ swz(r): 16 consecutive rows of one chunk
   // (one LDS cycle of a 16-byte read) fall on 16 distinct bank groups.
   __device__ __forceinline__ static int swz(int r) {
-    return RB == 64 ? (r ^ (r >> 2)) & 3 : RB == 128 ? (r >> 1) & 7 : r & 15;
+    return (r >> 1) & 7;
   }
 
   const ForwardArgs& args;
@@ -238,7 +231,7 @@ struct Gemm {
   // Byte offset of the lane's chunk inside the step, which depends on the LDS
   // block of the load modulo kVar: a few values for each operand.
   static constexpr int kRowsPer = 1024 / RB;   // rows of a load
-  static constexpr int kVar = RB == 64 ? 1 : 16 / kRowsPer;
+  static constexpr int kVar = 16 / kRowsPer;
   static constexpr int kVarA = std::min(kPwA, kVar), kVarB = std::min(kPwB, kVar);
   int cha[kVarA], chb[kVarB];
   uint32_t fa, fb;         // fragment base addresses (A rows, B rows of the wave)
@@ -357,12 +350,11 @@ struct Gemm {
   __device__ __forceinline__ static constexpr int spread(int i, int n, int span) {   // items before slot i
     return i >= span ? n : i * n / span;
   }
-  template <int PAR>
   __device__ __forceinline__ void round(int kt, int S, vec4u (&fa_)[MB], vec4u (&fb_)[2][NB],
-                                        Acc<MI> (&acc)[MB][NB]) {
+                                        f32x4 (&acc)[MB][NB]) {
     const int SN = S + 1 == NS ? 0 : S + 1, SP = S == 0 ? NS - 1 : S - 1;
     static_for<kSlices>([&](auto s_) __attribute__((always_inline)) {
-      constexpr int s = s_, cur = (s + PAR * kSlices) & 1;
+      constexpr int s = s_, cur = s & 1;
       constexpr bool last = s == kSlices - 1;
       if (last) {
         wait_loads_barrier<(NS - 2) * kLoads>();
@@ -373,7 +365,7 @@ struct Gemm {
       __builtin_amdgcn_s_setprio(1);
       static_for<N>([&](auto i_) __attribute__((always_inline)) {
         constexpr int i = i_, a = i / NB, b = i % NB;
-        acc[a][b] = mfma<T, MI>(fb_[cur][b], fa_[a], acc[a][b]);
+        acc[a][b] = mfma<T>(fb_[cur][b], fa_[a], acc[a][b]);
         if constexpr (b == NB - 1) fa_[a] = frag_a(from, at, a);
         // B fragments early, so that the next slice's first products have them
         constexpr int q0 = spread(i, NB, N / 2), q1 = spread(i + 1, NB, N / 2);
@@ -391,11 +383,11 @@ struct Gemm {
       __builtin_amdgcn_s_setprio(0);
     });
   }
-  __device__ __forceinline__ void mainloop(Acc<MI> (&acc)[MB][NB]) {
+  __device__ __forceinline__ void mainloop(f32x4 (&acc)[MB][NB]) {
 #pragma unroll
     for (int a = 0; a < MB; ++a)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) acc[a][b] = Acc<MI>{};
+      for (int b = 0; b < NB; ++b) acc[a][b] = f32x4{};
 #pragma unroll
     for (int d = 0; d < NS; ++d)
 #pragma unroll
@@ -407,13 +399,9 @@ struct Gemm {
 #pragma unroll
     for (int i = 0; i < NB; ++i) fb_[0][i] = frag_b(0, 0, i);
     int S = 0;
-    for (int kt = 0; kt < nk; kt += kUnroll) {
-      // where fragment sets alternate over two steps, one past the end
-      // multiplies zeros
-      static_for<kUnroll>([&](auto u) __attribute__((always_inline)) {
-        round<u>(kt + u, S, fa_, fb_, acc);
-        S = S + 1 == NS ? 0 : S + 1;
-      });
+    for (int kt = 0; kt < nk; ++kt) {
+      round(kt, S, fa_, fb_, acc);
+      S = S + 1 == NS ? 0 : S + 1;
     }
     wait_loads_barrier<0>();   // the stages become the epilogue's staging
   }
@@ -435,7 +423,7 @@ struct Gemm {
     }
   }
 
-  __device__ __forceinline__ void epilogue(const TileAt& at, const Acc<MI> (&acc)[MB][NB]) const {
+  __device__ __forceinline__ void epilogue(const TileAt& at, const f32x4 (&acc)[MB][NB]) const {
     const int F = GLU ? args.d_out / 2 : args.d_out;
     constexpr int wave_cols = GLU ? WC / 2 : WC;
     constexpr int lanes = wave_cols / UN;    // lanes of one row
@@ -460,16 +448,9 @@ struct Gemm {
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int h = 0; h < MI * MI / 256; ++h) {   // register quads: 4 columns of one row
-              const int col4 = b * MI + (MI == 32 ? 8 * h + 4 * (lane / 32) : 4 * (lane / 16));
-              f32x4 q;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) q[i] = acc[a + g][b][4 * h + i];
-              *reinterpret_cast<LDS_AS f32x4*>(
-                  (LDS_AS char*)(uintptr_t)(base + epi_off(g * MI + lane % MI, col4 / 4))) = q;
-            }
+          for (int b = 0; b < NB; ++b)   // a lane holds 4 columns of one row
+            *reinterpret_cast<LDS_AS f32x4*>((LDS_AS char*)(uintptr_t)(
+                base + epi_off(g * MI + lane % MI, b * (MI / 4) + lane / 16))) = acc[a + g][b];
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         for (int p = 0; p < 32 / per; ++p) {
@@ -517,7 +498,7 @@ __global__ __launch_bounds__(G::kThreads, G::kWavesPerSimd) void gemm_kernel(For
   TileAt at;
   if (!find_tile(args.seg, args.E, args.P, G::TM, cols, at)) return;
   G g(args, at, (LDS_AS char*)smem);
-  Acc<G::kMI> acc[G::kMB][G::kNB];
+  f32x4 acc[G::kMB][G::kNB];
   g.mainloop(acc);
   g.epilogue(at, acc);
 }
@@ -619,16 +600,16 @@ template <typename G>
 __device__ __forceinline__ void run_tile(const ForwardArgs& args, const TileAt& at,
                                          LDS_AS char* smem) {
   G g(args, at, smem);
-  Acc<G::kMI> acc[G::kMB][G::kNB];
+  f32x4 acc[G::kMB][G::kNB];
   g.mainloop(acc);
   g.epilogue(at, acc);
 }
 
 template <typename T, bool GLU>
 struct Ragged {
-  typedef Gemm<T, 16, 64, 128, 4, 2, 128, 2, GLU> G256;
-  typedef Gemm<T, 16, 64, 64, 2, 4, 128, 3, GLU> G128;
-  typedef Gemm<T, 16, 32, 64, 2, 4, 128, 3, GLU> G64;
+  typedef Gemm<T, 64, 128, 4, 2, 2, GLU> G256;
+  typedef Gemm<T, 64, 64, 2, 4, 3, GLU> G128;
+  typedef Gemm<T, 32, 64, 2, 4, 3, GLU> G64;
   static constexpr int kLds = std::max(std::max(G256::kLds, G128::kLds), G64::kLds);
   static constexpr int kThreads = G256::kThreads, kOut = G256::kOut;
 };
@@ -707,7 +688,7 @@ __global__ __launch_bounds__(256) void few_rows_kernel(ForwardArgs args, int col
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int c = 0; c < NC; ++c) acc[c] = mfma<T, 16>(w[u][c], x[u], acc[c]);
+      for (int c = 0; c < NC; ++c) acc[c] = mfma<T>(w[u][c], x[u], acc[c]);
 #pragma unroll
     for (int c = 0; c < NC; ++c) wp[c] += U * wstep[c];
     xp += U * xstep;
@@ -718,7 +699,7 @@ __global__ __launch_bounds__(256) void few_rows_kernel(ForwardArgs args, int col
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const vec4u w = *reinterpret_cast<const vec4u*>(in ? wp[c] : zero);
-      acc[c] = mfma<T, 16>(w, x, acc[c]);
+      acc[c] = mfma<T>(w, x, acc[c]);
       wp[c] += wstep[c];
     }
     xp += xstep;
@@ -820,21 +801,22 @@ int64_t expected(const ForwardArgs& a, int F, int tm, int out) {
 // without tiles, 12.3 with 32x64, 16.6 with 64x128, 34 with 256x256; 4
 // experts, 64 rows each: 25.1, 13.3, 16.9, 34; 4 experts, 512 rows each: 147,
 // 41, 24, 23; 16 experts, 512 rows each: 542, 149, 95, 71.
-template <typename T, bool GLU>
+template <bool GLU>
 hipError_t forward_bf16(const ForwardArgs& a, int F, bool far, hipStream_t s) {
+  typedef uint16_t T;
   constexpr int h = GLU ? 2 : 1;   // W rows of an output column
   if (expected(a, F, 16, 32 / h) <= 320) return launch_few_rows<T, 2, GLU>(a, F, s);
-  if (far) return launch_gemm<Gemm<T, 16, 32, 64, 2, 2, 128, 3, GLU, true>>(a, F, s);
+  if (far) return launch_gemm<Gemm<T, 32, 64, 2, 2, 3, GLU, true>>(a, F, s);
   // few rows for much W: wide tiles keep more of W in flight (16 experts of
   // 4096 columns and 2816 rows, 8 rows each: 67 us, 76 with the tiles below)
   if (a.P <= (int64_t)16 * a.E && expected(a, F, 32, 256 / h) >= 160)
-    return launch_gemm<Gemm<T, 16, 32, 64, 1, 4, 128, 4, GLU>>(a, F, s);
+    return launch_gemm<Gemm<T, 32, 64, 1, 4, 4, GLU>>(a, F, s);
   if (expected(a, F, 32, 64 / h) <= 320)
-    return launch_gemm<Gemm<T, 16, 32, 32, 1, 2, 128, 4, GLU>>(a, F, s);
+    return launch_gemm<Gemm<T, 32, 32, 1, 2, 4, GLU>>(a, F, s);
   if (expected(a, F, 64, 64 / h) <= 400)
-    return launch_gemm<Gemm<T, 16, 32, 32, 2, 2, 128, 3, GLU>>(a, F, s);
+    return launch_gemm<Gemm<T, 32, 32, 2, 2, 3, GLU>>(a, F, s);
   if (expected(a, F, 64, 128 / h) <= 512)
-    return launch_gemm<Gemm<T, 16, 32, 64, 2, 2, 128, 3, GLU>>(a, F, s);
+    return launch_gemm<Gemm<T, 32, 64, 2, 2, 3, GLU>>(a, F, s);
   return launch_ragged<T, GLU>(a, F, s);
 }
 
@@ -845,8 +827,8 @@ hipError_t forward_bf16(const ForwardArgs& a, int F, bool far, hipStream_t s) {
 template <bool GLU>
 hipError_t forward_f32(const ForwardArgs& a, int F, bool far, hipStream_t s) {
   if (expected(a, F, 16, GLU ? 16 : 32) <= 800) return launch_few_rows<float, 2, GLU>(a, F, s);
-  if (far) return launch_gemm<Gemm<float, 16, 32, 32, 2, 2, 128, 2, GLU, true>>(a, F, s);
-  return launch_gemm<Gemm<float, 16, 32, 32, 2, 2, 128, 2, GLU>>(a, F, s);
+  if (far) return launch_gemm<Gemm<float, 32, 32, 2, 2, 2, GLU, true>>(a, F, s);
+  return launch_gemm<Gemm<float, 32, 32, 2, 2, 2, GLU>>(a, F, s);
 }
 
 }  // namespace
@@ -861,8 +843,8 @@ hipError_t launch_grouped_forward(int dtype, const ForwardArgs& a, hipStream_t s
   const bool far = a.d_out * kbytes >= kNearBytes ||
                    (a.row_index != nullptr && a.T * kbytes >= kNearBytes);
   if (dtype == LRMOE_BF16)
-    return glu ? forward_bf16<uint16_t, true>(a, F, far, s)
-               : forward_bf16<uint16_t, false>(a, F, far, s);
+    return glu ? forward_bf16<true>(a, F, far, s)
+               : forward_bf16<false>(a, F, far, s);
   return glu ? forward_f32<true>(a, F, far, s) : forward_f32<false>(a, F, far, s);
 }
 

@@ -233,6 +233,24 @@ def test_route_sort_one_expert_and_odd_ids():
     assert out["counts"].tolist() == [0] * 7 + [10000]
 
 
+def test_route_sort_millions():
+    """More ids than 1024 workgroups take in one round, against torch's stable sort."""
+    T, K, E = 300_001, 8, 100
+    ids = torch.randint(-3, 140, (T, K), generator=gen(1), dtype=torch.int32).to(DEV)
+    w = torch.rand((T, K), device=DEV)
+    out = L.route_sort(ids, E, weights=w)
+    flat = ids.reshape(-1).long()
+    key, order = torch.sort(torch.where((flat >= 0) & (flat < E), flat, E), stable=True)
+    P = int((key < E).sum())
+    assert int(out["seg_offsets"][E]) == P
+    assert torch.equal(out["counts"], torch.bincount(key[:P], minlength=E))
+    assert torch.equal(out["row_index"][:P].long(), order[:P] // K)
+    assert (out["row_index"][P:] == -1).all() and (out["alpha"][P:] == 0).all()
+    assert torch.equal(out["alpha"][:P], w.reshape(-1)[order[:P]])
+    assert torch.equal(out["pos"].reshape(-1)[order[:P]].long(), torch.arange(P, device=DEV))
+    assert (out["pos"].reshape(-1)[order[P:]] == -1).all()
+
+
 ROWS = [(1, 1, 4, 8), (3, 2, 4, 16), (5, 8, 16, 264), (33, 3, 7, 1024), (9, 9, 20, 2056),
         (20, 17, 40, 40), (257, 4, 6, 512)]
 
