@@ -83,9 +83,8 @@ __device__ __forceinline__ int wave_scan(int x) {
 // Sigmoid from the hardware exp2 and reciprocal (about one ulp each; the
 // rounded argument adds |x| 2^-24 relative to exp(-x), which is at most 2^-25
 // of the result's scale).  exp(-x) = 2^(-x log2(e)); its overflow gives 0, as it
-// should.  expf and the exact division cost four times the instructions, which
-// bound the memory-bound kernels (the SwiGLU gradient of 32768 x 768: 78 us,
-// 59 us with these).
+// should.  expf and the exact division take several times the instructions, and
+// the elementwise kernels are near the point where those count.
 __device__ __forceinline__ float sigmoid_f32(float x) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * x));
 }

@@ -11,7 +11,21 @@
 // are and fragments are 16-byte LDS reads; the same kernel serves bfloat16
 // (v_mfma_f32_16x16x32_bf16, 8 values a fragment) and float32
 // (v_mfma_f32_16x16x4_f32, 4 values a fragment, four products), float32
-// accumulation in both.  Masked rows and the end of K read a page of zeros.
+// accumulation in both.  Masked rows and the end of K read zeros.
+//
+// What bounds it (one GPU's 16 experts, Zipf-shared pairs):
+//   many rows      the matrix cores: 8192^3 on one segment 810 us, 1.36 PFLOP/s
+//                  (torch.mm 1.41 to 1.55 on the same machines).  32768 pairs,
+//                  2048 -> 1536 SwiGLU with pre-activations 215 us, 0.96 PFLOP/s:
+//                  3.2 rounds of tiles, each with 6 us of tile search, row indices
+//                  and first loads ahead of it, and 150 MB of rows to write
+//   some rows      reading W: 2000 pairs over 369 MB of W 83 us (4.5 TB/s) when
+//                  evenly shared, 112 us with one expert of 591 rows, whose tiles
+//                  walk the same K with more to multiply
+//   few rows       one workgroup's walk over K: 2048 values take 7 to 9 us for 1
+//                  to 16 rows
+//   float32        the float32 matrix rate (157 TFLOP/s): 4097 pairs, 768 -> 2048
+//                  124 us, 104 TFLOP/s
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -188,7 +202,10 @@ __device__ __forceinline__ void wait_loads_barrier() {
 }
 
 // T: storage.  A wave computes WR x WC, WM x WN waves a workgroup, NS LDS
-// stages of one K step (128 bytes of every row) each.
+// stages of one K step (128 bytes of every row) each.  128 bytes are a cache
+// line: 64-byte steps with twice the stages were 5 to 15 % slower on every shape,
+// 256-byte ones with half the stages 10 to 25 % on all but the smallest.  Two
+// waves a SIMD: with one (128 x 128 a wave) the K loop ran 1.13 PFLOP/s on 8192^3.
 template <typename T, int WR, int WC, int WM, int WN, int NS, bool GLU, bool FAR = false>
 struct Gemm {
   static constexpr int MI = 16, RB = 128;                  // MFMA rows; row bytes of a K step
@@ -346,8 +363,12 @@ struct Gemm {
   // nobody reads buffer S any more; the loads of step kt + NS then go out
   // between the products.
   static constexpr int N = MB * NB;
+  // The loads of a step go out over the first half of the products after the
+  // barrier: over all of them they come too late for the next one (8192^3: 841
+  // us, 948 us over all, 851 us over a quarter).
   static constexpr int kSpan = N * kSlices / 2;
-  __device__ __forceinline__ static constexpr int spread(int i, int n, int span) {   // items before slot i
+  // Of n items spread over `span` slots, those before slot i.
+  __device__ __forceinline__ static constexpr int spread(int i, int n, int span) {
     return i >= span ? n : i * n / span;
   }
   __device__ __forceinline__ void round(int kt, int S, vec4u (&fa_)[MB], vec4u (&fb_)[2][NB],
@@ -508,7 +529,8 @@ __global__ __launch_bounds__(G::kThreads, G::kWavesPerSimd) void gemm_kernel(For
 // 128-row or 64-row code (an expert's last tile is half empty on average), and
 // the last round of an XCD's 32 CUs, if it would fill half of them or fewer, is
 // cut into 128-row or 64-row parts.  Whole tiles come first, then the ends,
-// each list in eighths over the XCDs.
+// each list in eighths over the XCDs.  (The training shape above: 237 us with
+// 256-row code alone, 215 us like this.)
 constexpr int kXcds = 8, kXcdCus = 32;
 
 __device__ __forceinline__ bool find_ragged_tile(const int32_t* seg, int E, int64_t P, int cols,
@@ -542,8 +564,9 @@ __device__ __forceinline__ bool find_ragged_tile(const int32_t* seg, int E, int6
   const int parts = __builtin_amdgcn_readlane(pend, 63);
   const int x = blockIdx.x % kXcds;
   const int64_t pos = blockIdx.x / kXcds;
-  const int64_t f0 = (int64_t)fulls * cols * x / kXcds, f1 = (int64_t)fulls * cols * (x + 1) / kXcds;
-  const int64_t p0 = (int64_t)parts * cols * x / kXcds, p1 = (int64_t)parts * cols * (x + 1) / kXcds;
+  const int64_t ft = (int64_t)fulls * cols, pt = (int64_t)parts * cols;
+  const int64_t f0 = ft * x / kXcds, f1 = ft * (x + 1) / kXcds;   // this XCD's share
+  const int64_t p0 = pt * x / kXcds, p1 = pt * (x + 1) / kXcds;
   const int64_t mine = f1 - f0 + p1 - p0;
   const int64_t rounds = mine / kXcdCus * kXcdCus;
   const int rem = (int)(mine - rounds);

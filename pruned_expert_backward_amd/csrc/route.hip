@@ -14,8 +14,10 @@
 //
 // All of them go by token (not by pair): the K rows of a token meet in one
 // wave, so x and dy are read once and a sum needs no atomics and has one
-// order.  They are bound by memory traffic.  A position outside 0..P-1 is
-// skipped.
+// order.  They are bound by memory traffic; a copy on this card moves 5.1 TB/s
+// (32768 tokens, 8 slots, rows of 2048 bf16: dispatch 231 us, 5.2 TB/s; combine
+// onto a residual 258 us, 5.2 TB/s; its gradient, 8191 tokens with rows of
+// 4096, 225 us, 5.1 TB/s).  A position outside 0..P-1 is skipped.
 #include "forward.h"
 
 namespace lrmoe {
@@ -29,7 +31,9 @@ namespace {
 // second walk over the ids, 64 at a time, ranks the lanes that hold the same
 // expert by ballots over the bits of the id.  Bin E holds the pairs of other
 // ranks.  Up to kOneBlock ids the one workgroup does it all in one launch
-// (a decoding step); more take a histogram launch first.
+// (64 tokens, 8 slots: 4.2 us); more take a histogram launch first (262144 ids
+// over 128 experts 12.6 us, of which the two launches are 5 and 8; 655360 ids 24
+// us; with 8192 ids a workgroup instead of 2048 20.5 and 27 us).
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kOneBlock = 4096;   // ids of a call that one workgroup sorts
@@ -79,7 +83,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_hist_kernel(const int32_t* 
   __syncthreads();
   const int64_t lo = blockIdx.x * per_block;
   const int64_t hi = lo + per_block < n ? lo + per_block : n;
-  for (int64_t i0 = lo + (tid & ~63); i0 < hi; i0 += kSortThreads) count(h, ids, i0 + (tid & 63), hi, E);
+  for (int64_t i0 = lo + (tid & ~63); i0 < hi; i0 += kSortThreads)
+    count(h, ids, i0 + (tid & 63), hi, E);
   __syncthreads();
   for (int e = tid; e <= E; e += kSortThreads) hist[(int64_t)blockIdx.x * (E + 1) + e] = h[e];
 }
@@ -268,7 +273,8 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = WEIGHTED ? fmaf(w[u], v[u][i], acc[i]) : acc[i] + v[u][i];
+        for (int i = 0; i < N; ++i)
+          acc[i] = WEIGHTED ? fmaf(w[u], v[u][i], acc[i]) : acc[i] + v[u][i];
     }
     store_vals(y + t * D + c, acc);
   }

@@ -713,7 +713,8 @@ def gate_topk(logits, k: int, score: int = GATE_SOFTMAX, select_bias=None, renor
         n = max(int(k), 0)
         out = dict(ids=_empty((T, n), torch.int32, dev), weights=_empty((T, n), torch.float32, dev))
     _call("lrmoe_gate_topk", dev, C.byref(g), _arg("logits", logits, logits.dtype, (T, E), dev),
-          None if select_bias is None else _arg("select_bias", select_bias, torch.float32, (E,), dev),
+          None if select_bias is None
+          else _arg("select_bias", select_bias, torch.float32, (E,), dev),
           _arg("ids", out["ids"], torch.int32, (T, int(k)), dev),
           _arg("weights", out["weights"], torch.float32, (T, int(k)), dev))
     return out
@@ -801,8 +802,8 @@ def dispatch_backward(dxp, pos, dtype: Optional[torch.dtype] = None, dx=None) ->
         dx = _empty((T, D), dtype or dxp.dtype, dev)
     elif dtype is not None and dx.dtype != dtype:
         raise TypeError(f"dx: {dtype} expected, got {dx.dtype}")
-    _call("lrmoe_dispatch_backward", dev, storage_dtype(dxp.dtype), storage_dtype(dx.dtype), T, K, D,
-          P, _arg("dxp", dxp, dxp.dtype, (P, D), dev), _arg("pos", pos, torch.int32, (T, K), dev),
+    _call("lrmoe_dispatch_backward", dev, storage_dtype(dxp.dtype), storage_dtype(dx.dtype), T, K,
+          D, P, _arg("dxp", dxp, dxp.dtype, (P, D), dev), _arg("pos", pos, torch.int32, (T, K), dev),
           _arg("dx", dx, dx.dtype, (T, D), dev))
     return dx
 
@@ -844,7 +845,8 @@ def combine_backward(dy, yp, pos, weights, out: Optional[dict] = None) -> dict:
 
 
 def grouped_forward(seg_offsets, x, W, row_index=None, bias=None, residual=None,
-                    act: int = ACT_NONE, save_pre: bool = False, out: Optional[dict] = None) -> dict:
+                    act: int = ACT_NONE, save_pre: bool = False,
+                    out: Optional[dict] = None) -> dict:
     """y_u = act(W_e x_row(u) + bias_e) + residual_u for the pairs of each
     segment of seg_offsets (device int32 [E + 1]).  x [T, d_in] is read through
     row_index [P] (None: row u of pair u), W is [E, d_out, d_in].  Returns y

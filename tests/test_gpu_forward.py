@@ -77,7 +77,8 @@ def test_gate(T, E, K, dt, score, renorm, biased):
 
 
 @pytest.mark.parametrize("dt", [F32, BF16])
-@pytest.mark.parametrize("score,biased", [("softmax", False), ("sigmoid", False), ("sigmoid", True)])
+@pytest.mark.parametrize("score,biased", [("softmax", False), ("sigmoid", False),
+                                          ("sigmoid", True)])
 def test_gate_ties_masks_and_extremes(dt, score, biased):
     inf, nan, low = float("inf"), float("nan"), torch.finfo(dt).min
     x = torch.zeros((10, 20))
