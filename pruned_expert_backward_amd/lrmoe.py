@@ -8,6 +8,7 @@ call raises.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -656,6 +657,11 @@ def _arg(name: str, t: torch.Tensor, dtype, shape, dev):
     raise ValueError(f"{name}: liblrmoe takes contiguous tensors")
 
 
+def _fresh(name: str, t: torch.Tensor, dtype, shape, dev):
+    """_arg for an output that the call has just made: nothing to check."""
+    return t.data_ptr() or None
+
+
 def _device(t: torch.Tensor):
     if not t.is_cuda:
         raise ValueError("liblrmoe takes device tensors")
@@ -709,14 +715,16 @@ def gate_topk(logits, k: int, score: int = GATE_SOFTMAX, select_bias=None, renor
     _rank("logits", logits, 2)
     T, E = logits.shape
     g = Gate(T, E, int(k), storage_dtype(logits.dtype), int(score), int(bool(renorm)), float(scale))
+    o = _fresh if out is None else _arg
     if out is None:
         n = max(int(k), 0)
-        out = dict(ids=_empty((T, n), torch.int32, dev), weights=_empty((T, n), torch.float32, dev))
+        out = dict(ids=torch.empty(T, n, dtype=torch.int32, device=dev),
+                   weights=torch.empty(T, n, dtype=torch.float32, device=dev))
     _call("lrmoe_gate_topk", dev, C.byref(g), _arg("logits", logits, logits.dtype, (T, E), dev),
           None if select_bias is None
           else _arg("select_bias", select_bias, torch.float32, (E,), dev),
-          _arg("ids", out["ids"], torch.int32, (T, int(k)), dev),
-          _arg("weights", out["weights"], torch.float32, (T, int(k)), dev))
+          o("ids", out["ids"], torch.int32, (T, int(k)), dev),
+          o("weights", out["weights"], torch.float32, (T, int(k)), dev))
     return out
 
 
@@ -729,16 +737,18 @@ def gate_topk_backward(logits, ids, dweights, score: int = GATE_SOFTMAX, renorm:
     T, E = logits.shape
     k = ids.shape[1]
     g = Gate(T, E, k, storage_dtype(logits.dtype), int(score), int(bool(renorm)), float(scale))
+    o = _fresh if dlogits is None else _arg
     if dlogits is None:
         dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
     _call("lrmoe_gate_topk_backward", dev, C.byref(g),
           _arg("logits", logits, logits.dtype, (T, E), dev),
           _arg("ids", ids, torch.int32, (T, k), dev),
           _arg("dweights", dweights, torch.float32, (T, k), dev),
-          _arg("dlogits", dlogits, logits.dtype, (T, E), dev))
+          o("dlogits", dlogits, logits.dtype, (T, E), dev))
     return dlogits
 
 
+@functools.lru_cache(maxsize=256)
 def route_sort_workspace_bytes(T: int, K: int, E: int) -> int:
     n = C.c_size_t(0)
     check("lrmoe_route_sort_workspace", lib().lrmoe_route_sort_workspace(T, K, E, C.byref(n)))
@@ -754,22 +764,23 @@ def route_sort(ids, E: int, weights=None, out: Optional[dict] = None, ws=None) -
     _rank("ids", ids, 2)
     T, K = ids.shape
     need = route_sort_workspace_bytes(T, K, int(E))
+    o = _fresh if out is None else _arg
     if out is None:
-        out = dict(counts=_empty((E,), torch.int64, dev),
-                   seg_offsets=_empty((E + 1,), torch.int32, dev),
-                   row_index=_empty((T * K,), torch.int32, dev),
-                   pos=_empty((T, K), torch.int32, dev))
+        out = dict(counts=torch.empty(E, dtype=torch.int64, device=dev),
+                   seg_offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
+                   row_index=torch.empty(T * K, dtype=torch.int32, device=dev),
+                   pos=torch.empty(T, K, dtype=torch.int32, device=dev))
         if weights is not None:
-            out["alpha"] = _empty((T * K,), torch.float32, dev)
+            out["alpha"] = torch.empty(T * K, dtype=torch.float32, device=dev)
     addr, n, _keep = _workspace(need, ws, dev)
     alpha = out.get("alpha")
     _call("lrmoe_route_sort", dev, T, K, int(E), _arg("ids", ids, torch.int32, (T, K), dev),
           None if weights is None else _arg("weights", weights, torch.float32, (T, K), dev),
-          _arg("counts", out["counts"], torch.int64, (E,), dev),
-          _arg("seg_offsets", out["seg_offsets"], torch.int32, (E + 1,), dev),
-          _arg("row_index", out["row_index"], torch.int32, (T * K,), dev),
-          _arg("pos", out["pos"], torch.int32, (T, K), dev),
-          None if alpha is None else _arg("alpha", alpha, torch.float32, (T * K,), dev),
+          o("counts", out["counts"], torch.int64, (E,), dev),
+          o("seg_offsets", out["seg_offsets"], torch.int32, (E + 1,), dev),
+          o("row_index", out["row_index"], torch.int32, (T * K,), dev),
+          o("pos", out["pos"], torch.int32, (T, K), dev),
+          None if alpha is None else o("alpha", alpha, torch.float32, (T * K,), dev),
           addr, n)
     return out
 
@@ -782,12 +793,13 @@ def dispatch(x, pos, xp=None) -> torch.Tensor:
     _rank("pos", pos, 2)
     T, D = x.shape
     K = pos.shape[1]
+    o = _fresh if xp is None else _arg
     if xp is None:
-        xp = _empty((T * K, D), x.dtype, dev)
+        xp = torch.empty(T * K, D, dtype=x.dtype, device=dev)
     P = xp.shape[0]
     _call("lrmoe_dispatch", dev, storage_dtype(x.dtype), T, K, D, P,
           _arg("x", x, x.dtype, (T, D), dev), _arg("pos", pos, torch.int32, (T, K), dev),
-          _arg("xp", xp, x.dtype, (P, D), dev))
+          o("xp", xp, x.dtype, (P, D), dev))
     return xp
 
 
@@ -798,13 +810,14 @@ def dispatch_backward(dxp, pos, dtype: Optional[torch.dtype] = None, dx=None) ->
     _rank("pos", pos, 2)
     P, D = dxp.shape
     T, K = pos.shape
+    o = _fresh if dx is None else _arg
     if dx is None:
-        dx = _empty((T, D), dtype or dxp.dtype, dev)
+        dx = torch.empty(T, D, dtype=dtype or dxp.dtype, device=dev)
     elif dtype is not None and dx.dtype != dtype:
         raise TypeError(f"dx: {dtype} expected, got {dx.dtype}")
     _call("lrmoe_dispatch_backward", dev, storage_dtype(dxp.dtype), storage_dtype(dx.dtype), T, K,
           D, P, _arg("dxp", dxp, dxp.dtype, (P, D), dev), _arg("pos", pos, torch.int32, (T, K), dev),
-          _arg("dx", dx, dx.dtype, (T, D), dev))
+          o("dx", dx, dx.dtype, (T, D), dev))
     return dx
 
 
@@ -815,13 +828,14 @@ def combine(yp, pos, weights, residual=None, y=None) -> torch.Tensor:
     _rank("pos", pos, 2)
     P, D = yp.shape
     T, K = pos.shape
+    o = _fresh if y is None else _arg
     if y is None:
-        y = _empty((T, D), yp.dtype, dev)
+        y = torch.empty(T, D, dtype=yp.dtype, device=dev)
     _call("lrmoe_combine", dev, storage_dtype(yp.dtype), T, K, D, P,
           _arg("yp", yp, yp.dtype, (P, D), dev), _arg("pos", pos, torch.int32, (T, K), dev),
           _arg("weights", weights, torch.float32, (T, K), dev),
           None if residual is None else _arg("residual", residual, yp.dtype, (T, D), dev),
-          _arg("y", y, yp.dtype, (T, D), dev))
+          o("y", y, yp.dtype, (T, D), dev))
     return y
 
 
@@ -833,14 +847,16 @@ def combine_backward(dy, yp, pos, weights, out: Optional[dict] = None) -> dict:
     _rank("pos", pos, 2)
     P, D = yp.shape
     T, K = pos.shape
+    o = _fresh if out is None else _arg
     if out is None:
-        out = dict(dyp=_empty((P, D), yp.dtype, dev), dweights=_empty((T, K), torch.float32, dev))
+        out = dict(dyp=torch.empty(P, D, dtype=yp.dtype, device=dev),
+                   dweights=torch.empty(T, K, dtype=torch.float32, device=dev))
     _call("lrmoe_combine_backward", dev, storage_dtype(yp.dtype), T, K, D, P,
           _arg("dy", dy, yp.dtype, (T, D), dev), _arg("yp", yp, yp.dtype, (P, D), dev),
           _arg("pos", pos, torch.int32, (T, K), dev),
           _arg("weights", weights, torch.float32, (T, K), dev),
-          _arg("dyp", out["dyp"], yp.dtype, (P, D), dev),
-          _arg("dweights", out["dweights"], torch.float32, (T, K), dev))
+          o("dyp", out["dyp"], yp.dtype, (P, D), dev),
+          o("dweights", out["dweights"], torch.float32, (T, K), dev))
     return out
 
 
@@ -861,12 +877,13 @@ def grouped_forward(seg_offsets, x, W, row_index=None, bias=None, residual=None,
     P = T if row_index is None else row_index.numel()
     glu = act == ACT_SWIGLU
     F = d_out // 2 if glu else d_out
+    o = _fresh if out is None else _arg
     if out is None:
-        out = dict(y=_empty((P, F), dt, dev))
+        out = dict(y=torch.empty(P, F, dtype=dt, device=dev))
         if save_pre:
-            out["pre_a"] = _empty((P, F), dt, dev)
+            out["pre_a"] = torch.empty(P, F, dtype=dt, device=dev)
             if glu:
-                out["pre_b"] = _empty((P, F), dt, dev)
+                out["pre_b"] = torch.empty(P, F, dtype=dt, device=dev)
     fw = Forward(E, storage_dtype(dt), P, T, d_out, d_in, int(act))
     pa, pb = out.get("pre_a"), out.get("pre_b")
     _call("lrmoe_grouped_forward", dev, C.byref(fw),
@@ -875,9 +892,9 @@ def grouped_forward(seg_offsets, x, W, row_index=None, bias=None, residual=None,
           _arg("x", x, dt, (T, d_in), dev), _arg("W", W, dt, (E, d_out, d_in), dev),
           None if bias is None else _arg("bias", bias, dt, (E, d_out), dev),
           None if residual is None else _arg("residual", residual, dt, (P, F), dev),
-          _arg("y", out["y"], dt, (P, F), dev),
-          None if pa is None else _arg("pre_a", pa, dt, (P, F), dev),
-          None if pb is None else _arg("pre_b", pb, dt, (P, F), dev))
+          o("y", out["y"], dt, (P, F), dev),
+          None if pa is None else o("pre_a", pa, dt, (P, F), dev),
+          None if pb is None else o("pre_b", pb, dt, (P, F), dev))
     return out
 
 
@@ -893,9 +910,11 @@ def act_backward(seg_offsets, dy, pre_a=None, pre_b=None, act: int = ACT_NONE, d
     P, F = dy.shape
     E, dt = seg_offsets.numel() - 1, dy.dtype
     d_out = 2 * F if act == ACT_SWIGLU else F
+    o = _fresh if out is None else _arg
     if out is None:
-        out = dict(dz=_empty((P, d_out), dz_dtype or dt, dev),
-                   dbias=_empty((E, d_out), torch.float32, dev) if dbias else None)
+        out = dict(dz=torch.empty(P, d_out, dtype=dz_dtype or dt, device=dev),
+                   dbias=(torch.empty(E, d_out, dtype=torch.float32, device=dev) if dbias
+                          else None))
     dz, db = out["dz"], out.get("dbias")
     # d_in plays no part here; any row length the library takes
     fw = Forward(E, storage_dtype(dt), P, P, d_out, 8, int(act))
@@ -909,6 +928,6 @@ def act_backward(seg_offsets, dy, pre_a=None, pre_b=None, act: int = ACT_NONE, d
           _arg("dy", dy, dt, (P, F), dev),
           None if pre_a is None else _arg("pre_a", pre_a, dt, (P, F), dev),
           None if pre_b is None else _arg("pre_b", pre_b, dt, (P, F), dev),
-          _arg("dz", dz, dz.dtype, (P, d_out), dev),
-          None if db is None else _arg("dbias", db, torch.float32, (E, d_out), dev), addr, n)
+          o("dz", dz, dz.dtype, (P, d_out), dev),
+          None if db is None else o("dbias", db, torch.float32, (E, d_out), dev), addr, n)
     return out
