@@ -181,7 +181,7 @@ __device__ __forceinline__ float unordered(uint32_t o) {
 // keys that are only nearly exact.  Rounds go on past K while a key is within
 // 2^-19 (1 + the larger magnitude) of the one before it, or not ordered with
 // it; `close` tells whether there were such neighbours at all, and `found` how
-// many experts the lanes hold (LANES: perhaps not all that are near).
+// many experts the lanes hold (LANES + 1: more are near than there are lanes).
 template <int LANES, int V, bool CHECK>
 __device__ __forceinline__ int select(uint32_t (&key)[V], int l, int K, bool& close, int& found) {
   int mine = -1;   // lane k keeps the expert of round k
@@ -189,7 +189,7 @@ __device__ __forceinline__ int select(uint32_t (&key)[V], int l, int K, bool& cl
   const int first = expert_of<LANES, V>(l, 0);
   close = false;
   int k = 0;
-  for (; k < (CHECK ? LANES : K); ++k) {
+  for (; k < (CHECK ? LANES + 1 : K); ++k) {
     uint32_t best = key[0];
 #pragma unroll
     for (int v = 1; v < V; ++v) best = max(best, key[v]);
@@ -305,7 +305,7 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(
       // float32 keys are within 2^-21 (1 + |key|) of the float64 ones (sigmoid
       // to 2^-22, the sum's rounding 2^-24 |key|): neighbours further apart
       // than that are in float64's order.  This row has some that are not.
-      if (found < LANES) {   // all that matter are here, one a lane
+      if (found <= LANES) {   // all that matter are here, one a lane
         double k = -__builtin_inf();
         if (mine >= 0) k = exact_key(logit(row, mine), bias[mine]);
         mine = reorder<LANES>(k, mine, l, found);

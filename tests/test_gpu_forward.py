@@ -141,6 +141,26 @@ def test_gate_near_keys(E, K):
     assert torch.equal(out["ids"].cpu().long(), ids)
 
 
+@pytest.mark.parametrize("E,K", [(40, 15), (40, 16), (256, 16), (64, 17), (300, 63), (300, 64),
+                                 (16, 16), (128, 1)])
+def test_gate_near_keys_at_the_last_slot(E, K):
+    """All keys far apart but those of ranks K and K + 1, which one float32 sum
+    rounds to the same number: the one a float32 step larger is chosen, though
+    its expert is the higher one."""
+    x = torch.zeros((1, E))                                  # sigmoid 1/2, exactly
+    bias = 0.45 - 0.002 * torch.arange(E, dtype=torch.float32) * (256 / max(E, 256))
+    if K < E:
+        for _ in range(64):   # a step up that float32's 1/2 + bias does not see
+            bias[K] = torch.nextafter(bias[K - 1], torch.tensor(1.0))
+            if 0.5 + bias[K] == 0.5 + bias[K - 1]:
+                break
+            bias[K - 1] = torch.nextafter(bias[K - 1], torch.tensor(-1.0))
+        assert 0.5 + bias[K] == 0.5 + bias[K - 1] and bias[K] > bias[K - 1]
+    ids, _ = O.gate(x, K, "sigmoid", bias)
+    out = L.gate_topk(x.to(DEV), K, score=L.GATE_SIGMOID, select_bias=bias.to(DEV))
+    assert torch.equal(out["ids"].cpu().long(), ids)
+
+
 @pytest.mark.parametrize("T,E,K", GATE)
 @pytest.mark.parametrize("dt", [F32, BF16])
 @pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False),
