@@ -1,7 +1,5 @@
 // C-ABI entry points of the forward side: argument checks, then one launcher
 // each.
-#include <string.h>
-
 #include "checks.h"
 #include "forward.h"
 

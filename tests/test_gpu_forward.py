@@ -492,6 +492,23 @@ def test_linear_tiles_of_rows_beyond_32_bits(dt, T):
     within(y, ref["y"], ez + HALF[dt] * (ref["y"].abs() + ez), "y")
 
 
+def test_linear_expert_beyond_a_buffer():
+    """One expert's weights of more than 2 GiB: its last and first columns."""
+    d_in, d_out, n = 32768, 32776, 130
+    W = torch.zeros((1, d_out, d_in), dtype=BF16, device=DEV)
+    ends = normal(gen(9), (2, 16, d_in), BF16, 0.1)
+    W[0, :16], W[0, -16:] = ends[0].to(DEV), ends[1].to(DEV)
+    x = normal(gen(10), (n, d_in), BF16)
+    for rows in (1, n):
+        seg = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+        y = L.grouped_forward(seg, x[:rows].to(DEV).contiguous(), W)["y"]
+        for part, got in ((ends[0], y[:, :16]), (ends[1], y[:, -16:])):
+            ref = O.linear([0, rows], x[:rows], part[None])
+            ez = (d_in + 2) * 2 * U * ref["mag"]
+            within(got, ref["y"], ez + HALF[BF16] * (ref["y"].abs() + ez), "y")
+        assert (y[:, 16:-16] == 0).all()
+
+
 def test_linear_rows_in_any_batch_company():
     """NaN rows of one expert or token touch no other row."""
     seg = zipf_seg(2500, 4)
