@@ -335,15 +335,18 @@ struct Gemm {
     const int blk = isA ? wave * kPwA + j : wave * kPwB + j - kPwA;
     const uint32_t dst =
         __builtin_amdgcn_readfirstlane(lds + buf * kStage + (isA ? 0 : TM * RB) + blk * 1024);
-    // uniform: the K step read (steps go round from k0), bytes left from there
-    const int k = kt + k0 < nk ? kt + k0 : kt + k0 - nk;
-    const int left = kt < nk ? kbytes - k * RB : 0;
+    // uniform: where the K step read starts (steps go round from k0), bytes left
+    // from there.  Past the end of K it is 0: a load is out of range when its lane
+    // offset reaches the buffer's size less the scalar offset, and a step behind nk
+    // can lie past a buffer of one row, where that difference would be negative.
+    const int at = kt >= nk ? 0 : (kt + k0 < nk ? kt + k0 : kt + k0 - nk) * RB;
+    const int left = kt < nk ? kbytes - at : 0;
     const bool in = chunk_of(j) < left;
     if constexpr (FAR) {
       load_lds16(dst, in ? src[j] : reinterpret_cast<const char*>(zero_page));
       src[j] += step[j];
     } else {
-      load_lds16(dst, isA ? xbuf : wbuf, in ? off[j] : kOutOfRange, k * RB);
+      load_lds16(dst, isA ? xbuf : wbuf, in ? off[j] : kOutOfRange, at);
     }
   }
 
