@@ -668,19 +668,18 @@ def _device(t: torch.Tensor):
     return t.device
 
 
-# The current stream's handle without a Stream object around it (2 us a call).
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
 def _call(fn: str, dev, *args) -> None:
     """Run an entry point on `dev` (its last argument, the stream, is added)."""
     f = getattr(_lib_handle or lib(), fn)
+    # The current stream's handle without a Stream object around it (2 us a
+    # call).  Looked up here: a CPU build of torch does not have it.
+    raw_stream = torch._C._cuda_getCurrentRawStream
     at = dev.index
     if at == torch.cuda.current_device():
-        st = f(*args, _raw_stream(at))
+        st = f(*args, raw_stream(at))
     else:
         with torch.cuda.device(dev):
-            st = f(*args, _raw_stream(at))
+            st = f(*args, raw_stream(at))
     if st != 0:
         check(fn, st)
 
