@@ -64,7 +64,7 @@
 extern "C" {
 #endif
 
-#define LRMOE_ABI_VERSION 4
+#define LRMOE_ABI_VERSION 5
 #define LRMOE_MAX_EXPERTS 256
 
 typedef enum {

@@ -26,7 +26,7 @@ ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_SWIGLU = 0, 1, 2, 3, 4
 MAX_EXPERTS = 256
 MAX_GATE_EXPERTS = 1024
 MAX_TOPK = 64
-ABI_VERSION = 4
+ABI_VERSION = 5
 
 STATUS = {0: "LRMOE_OK", 1: "LRMOE_ERR_NULL", 2: "LRMOE_ERR_INVALID", 3: "LRMOE_ERR_SHAPE",
           4: "LRMOE_ERR_ALIGN", 5: "LRMOE_ERR_DTYPE", 6: "LRMOE_ERR_WORKSPACE",
@@ -94,6 +94,8 @@ def lib() -> C.CDLL:
                            "`python -m pruned_expert_backward_amd.build`")
     L = C.CDLL(LIB_PATH)
     L.lrmoe_abi_version.restype = C.c_int32
+    if L.lrmoe_abi_version() != ABI_VERSION:   # before any symbol that it may lack
+        raise RuntimeError("liblrmoe ABI version mismatch; rebuild the library")
     L.lrmoe_status_string.restype = C.c_char_p
     L.lrmoe_status_string.argtypes = [C.c_int]
     L.lrmoe_plan_quota.restype = C.c_int
@@ -162,8 +164,6 @@ def lib() -> C.CDLL:
             ("lrmoe_act_backward", [C.POINTER(Forward), i32] + [_P] * 7 + [C.c_size_t, _P])):
         fn = getattr(L, name)
         fn.restype, fn.argtypes = C.c_int, args
-    if L.lrmoe_abi_version() != ABI_VERSION:
-        raise RuntimeError("liblrmoe ABI version mismatch; rebuild the library")
     _lib_handle = L
     return L
 

@@ -3,6 +3,7 @@ library that does not fit."""
 import os
 import subprocess
 import sys
+import types
 
 import pytest
 
@@ -27,3 +28,15 @@ def test_host_side_without_cuda_streams_in_torch():
                "print(L.plan_quota([10, 0, 5], ('ratio', 4, 5)))")
     assert r.returncode == 0, r.stderr
     assert r.stdout.strip() == str(L.plan_quota([10, 0, 5], ("ratio", 4, 5)))
+
+
+def test_library_of_an_older_version_is_named_as_such(monkeypatch):
+    """Version 4 has no forward side: loading it says what to do, and does not
+    end at the first symbol that it lacks."""
+    def version():
+        return 4
+
+    monkeypatch.setattr(L, "_lib_handle", None)
+    monkeypatch.setattr(L.C, "CDLL", lambda path: types.SimpleNamespace(lrmoe_abi_version=version))
+    with pytest.raises(RuntimeError, match="rebuild"):
+        L.lib()
