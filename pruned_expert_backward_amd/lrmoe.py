@@ -699,6 +699,13 @@ def _workspace(need: int, ws: Optional[torch.Tensor], dev):
     return (ws.data_ptr() if n else None), n, ws
 
 
+def _asked(option: str, out: dict, *names: str):
+    """Refuse an option whose results a caller's out has no buffers for."""
+    for name in names:
+        if out.get(name) is None:
+            raise ValueError(f"{option}: out holds no {name}")
+
+
 def _rank(name: str, t: torch.Tensor, n: int):
     if t.dim() != n:
         raise ValueError(f"{name}: {n} dimensions expected, got {t.dim()}")
@@ -758,7 +765,7 @@ def route_sort(ids, E: int, weights=None, out: Optional[dict] = None, ws=None) -
     """Stable sort of the slots of ids [T, K] by expert: counts int64 [E],
     seg_offsets int32 [E + 1], row_index int32 [T * K] (token of each pair),
     pos int32 [T, K] (place of each slot, -1 for ids outside 0..E-1) and, with
-    weights [T, K], alpha float32 [T * K]."""
+    weights [T, K], alpha float32 [T * K], which a given out then holds too."""
     dev = _device(ids)
     _rank("ids", ids, 2)
     T, K = ids.shape
@@ -771,6 +778,8 @@ def route_sort(ids, E: int, weights=None, out: Optional[dict] = None, ws=None) -
                    pos=torch.empty(T, K, dtype=torch.int32, device=dev))
         if weights is not None:
             out["alpha"] = torch.empty(T * K, dtype=torch.float32, device=dev)
+    elif weights is not None:
+        _asked("weights", out, "alpha")
     addr, n, _keep = _workspace(need, ws, dev)
     alpha = out.get("alpha")
     _call("lrmoe_route_sort", dev, T, K, int(E), _arg("ids", ids, torch.int32, (T, K), dev),
@@ -866,8 +875,8 @@ def grouped_forward(seg_offsets, x, W, row_index=None, bias=None, residual=None,
     segment of seg_offsets (device int32 [E + 1]).  x [T, d_in] is read through
     row_index [P] (None: row u of pair u), W is [E, d_out, d_in].  Returns y
     [P, F] (F = d_out, or d_out / 2 for ACT_SWIGLU) and, with save_pre, the
-    pre-activations pre_a (and pre_b).  Rows behind the last segment are left
-    as they were."""
+    pre-activations pre_a (and pre_b); where out is given, those are stored
+    that it holds.  Rows behind the last segment are left as they were."""
     dev = _device(x)
     _rank("x", x, 2)
     _rank("W", W, 3)
@@ -883,6 +892,8 @@ def grouped_forward(seg_offsets, x, W, row_index=None, bias=None, residual=None,
             out["pre_a"] = torch.empty(P, F, dtype=dt, device=dev)
             if glu:
                 out["pre_b"] = torch.empty(P, F, dtype=dt, device=dev)
+    elif save_pre:
+        _asked("save_pre", out, *(("pre_a", "pre_b") if glu else ("pre_a",)))
     fw = Forward(E, storage_dtype(dt), P, T, d_out, d_in, int(act))
     pa, pb = out.get("pre_a"), out.get("pre_b")
     _call("lrmoe_grouped_forward", dev, C.byref(fw),
@@ -897,13 +908,14 @@ def grouped_forward(seg_offsets, x, W, row_index=None, bias=None, residual=None,
     return out
 
 
-def act_backward(seg_offsets, dy, pre_a=None, pre_b=None, act: int = ACT_NONE, dbias: bool = True,
-                 dz_dtype: Optional[torch.dtype] = None, out: Optional[dict] = None,
-                 ws=None) -> dict:
+def act_backward(seg_offsets, dy, pre_a=None, pre_b=None, act: int = ACT_NONE,
+                 dbias: Optional[bool] = None, dz_dtype: Optional[torch.dtype] = None,
+                 out: Optional[dict] = None, ws=None) -> dict:
     """Gradient of grouped_forward's epilogue: dz [P, d_out] (gate half first
     for ACT_SWIGLU; type dz_dtype, default dy's) and dbias float32 [E, d_out]
-    (None without).  dz then goes through grouped_backward with quotas =
-    counts, or as float32 through grouped_backward_gate_up."""
+    (None with dbias=False); where out is given, dbias is computed if it holds
+    one.  dz then goes through grouped_backward with quotas = counts, or as
+    float32 through grouped_backward_gate_up."""
     dev = _device(dy)
     _rank("dy", dy, 2)
     P, F = dy.shape
@@ -912,8 +924,13 @@ def act_backward(seg_offsets, dy, pre_a=None, pre_b=None, act: int = ACT_NONE, d
     o = _fresh if out is None else _arg
     if out is None:
         out = dict(dz=torch.empty(P, d_out, dtype=dz_dtype or dt, device=dev),
-                   dbias=(torch.empty(E, d_out, dtype=torch.float32, device=dev) if dbias
-                          else None))
+                   dbias=(torch.empty(E, d_out, dtype=torch.float32, device=dev)
+                          if dbias is None or dbias else None))
+    else:
+        if dbias:
+            _asked("dbias", out, "dbias")
+        if dz_dtype is not None and out["dz"].dtype != dz_dtype:
+            raise TypeError(f"dz: {dz_dtype} expected, got {out['dz'].dtype}")
     dz, db = out["dz"], out.get("dbias")
     # d_in plays no part here; any row length the library takes
     fw = Forward(E, storage_dtype(dt), P, P, d_out, 8, int(act))
