@@ -70,17 +70,17 @@ __device__ __forceinline__ bool find_run(const int32_t* seg, int E, int64_t P, i
   return true;
 }
 
+// SiLU' or GELU'.
 template <int ACT>
 __device__ __forceinline__ float act_grad(float a) {
-  if constexpr (ACT == LRMOE_ACT_RELU) return a > 0.f ? 1.f : 0.f;
-  if constexpr (ACT == LRMOE_ACT_SILU || ACT == LRMOE_ACT_SWIGLU) {
+  static_assert(ACT == LRMOE_ACT_SILU || ACT == LRMOE_ACT_GELU, "the others have no function");
+  if constexpr (ACT == LRMOE_ACT_SILU) {
     const float s = sigmoid_f32(a);
     return s + a * s * (1.f - s);
-  }
-  if constexpr (ACT == LRMOE_ACT_GELU)
+  } else {
     return 0.5f * (1.f + erff(a * 0.70710678f)) +
            a * (0.39894228f * __builtin_amdgcn_exp2f(-0.72134752f * a * a));   // exp(-a^2 / 2)
-  return 1.f;
+  }
 }
 
 template <typename T, typename TO, int N, int ACT, int LPR>
@@ -246,8 +246,8 @@ hipError_t run(int act, const int32_t* seg, const void* dy, const void* a, const
 
 }  // namespace
 
-size_t act_backward_workspace(int64_t P, int32_t E, int32_t width, bool dbias) {
-  return dbias ? (size_t)max_runs(P, E) * width * sizeof(float) : 0;
+size_t act_backward_workspace(int64_t P, int32_t E, int32_t width) {
+  return (size_t)max_runs(P, E) * width * sizeof(float);
 }
 
 hipError_t launch_act_backward(int dtype, int out_dtype, int act, const int32_t* seg,

@@ -208,7 +208,7 @@ lrmoe_status lrmoe_grouped_forward(const lrmoe_forward* fw, const int32_t* seg_o
 lrmoe_status lrmoe_act_backward_workspace(const lrmoe_forward* fw, size_t* bytes_out) {
   if (bytes_out == nullptr) return LRMOE_ERR_NULL;
   LRMOE_TRY(check_forward(fw));
-  *bytes_out = act_backward_workspace(fw->P, fw->E, fw->d_out, true);
+  *bytes_out = act_backward_workspace(fw->P, fw->E, fw->d_out);
   return LRMOE_OK;
 }
 
@@ -227,7 +227,7 @@ lrmoe_status lrmoe_act_backward(const lrmoe_forward* fw, int32_t dz_dtype,
   LRMOE_TRY(need(dz, fw->P));
   LRMOE_TRY(optional(dbias));
   if (dbias != nullptr) {
-    const size_t ws = act_backward_workspace(fw->P, fw->E, fw->d_out, true);
+    const size_t ws = act_backward_workspace(fw->P, fw->E, fw->d_out);
     LRMOE_TRY(need(workspace, (int64_t)ws));
     if (ws_bytes < ws) return LRMOE_ERR_WORKSPACE;
   }

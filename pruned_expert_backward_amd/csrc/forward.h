@@ -129,7 +129,7 @@ struct ForwardArgs {
 };
 hipError_t launch_grouped_forward(int dtype, const ForwardArgs& a, hipStream_t s);
 
-size_t act_backward_workspace(int64_t P, int32_t E, int32_t width, bool dbias);
+size_t act_backward_workspace(int64_t P, int32_t E, int32_t width);  // with bias sums
 hipError_t launch_act_backward(int dtype, int out_dtype, int act, const int32_t* seg,
                                const void* dy, const void* a, const void* b, int64_t P, int32_t E,
                                int32_t F, void* dz, float* dbias, float* ws, hipStream_t s);

@@ -371,13 +371,14 @@ struct Gemm {
   // barrier: over all of them they come too late for the next one (8192^3: 841
   // us, 948 us over all, 851 us over a quarter).
   static constexpr int kSpan = N * kSlices / 2;
+  static_assert(kSpan <= N, "all loads of a step in its last slice");
   // Of n items spread over `span` slots, those before slot i.
   __device__ __forceinline__ static constexpr int spread(int i, int n, int span) {
     return i >= span ? n : i * n / span;
   }
   __device__ __forceinline__ void round(int kt, int S, vec4u (&fa_)[MB], vec4u (&fb_)[2][NB],
                                         f32x4 (&acc)[MB][NB]) {
-    const int SN = S + 1 == NS ? 0 : S + 1, SP = S == 0 ? NS - 1 : S - 1;
+    const int SN = S + 1 == NS ? 0 : S + 1;
     static_for<kSlices>([&](auto s_) __attribute__((always_inline)) {
       constexpr int s = s_, cur = s & 1;
       constexpr bool last = s == kSlices - 1;
@@ -397,12 +398,12 @@ struct Gemm {
         static_for<q1 - q0>([&](auto q) __attribute__((always_inline)) {
           fb_[cur ^ 1][q0 + q] = frag_b(from, at, q0 + q);
         });
-        constexpr int slot = last ? i : (s + 1) * N + i;   // counted from the barrier
-        constexpr int l0 = spread(slot, kLoads, kSpan), l1 = spread(slot + 1, kLoads, kSpan);
-        static_for<l1 - l0>([&](auto q) __attribute__((always_inline)) {
-          if (last) issue(l0 + q, S, kt + NS);
-          else if (kt > 0) issue(l0 + q, SP, kt + NS - 1);
-        });
+        if constexpr (last) {
+          constexpr int l0 = spread(i, kLoads, kSpan), l1 = spread(i + 1, kLoads, kSpan);
+          static_for<l1 - l0>([&](auto q) __attribute__((always_inline)) {
+            issue(l0 + q, S, kt + NS);
+          });
+        }
         __builtin_amdgcn_sched_barrier(0);
       });
       __builtin_amdgcn_s_setprio(0);
