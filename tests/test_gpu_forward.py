@@ -412,8 +412,8 @@ def check_linear(seg, x, W, row, bias, res, name, pre, P=None):
     return out
 
 
-# segments; the mean rows of an expert choose the variant (8 and fewer: no
-# tiles; below 256: 128-row tiles; else 256-row tiles)
+# segments; most calls have few enough workgroups to do without tiles (tile
+# shapes: the widest of the last ones here, below, test_gpu_forward_tiles.py)
 SEGS = [[0, 1], [0, 0, 0, 1], [0, 3, 3, 20, 21], [0, 16, 33], [0, 40, 41, 41, 170],
         [0, 127, 255, 384], [0, 300], [0, 5, 600, 1100], [0, 0, 0]]
 DIMS = [(8, 8), (24, 40), (64, 136), (72, 264), (264, 520)]
