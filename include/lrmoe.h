@@ -466,8 +466,14 @@ lrmoe_status lrmoe_grouped_backward_gate_up_timed(
  * aligned, row lengths multiples of 8 (bf16) or 4 (float32), outputs not
  * aliasing inputs, nothing allocated, errors before any launch).  Expert
  * counts and segments stay on the device: nothing visits the host between
- * these calls, so a whole layer can be captured in a graph.  A graph that is
- * replayed beside other calls needs a workspace of its own.
+ * these calls, so a layer's forward and the gradients declared here can be
+ * captured in a graph.  (The products' gradients take counts and quotas from
+ * the host, as all of the pruned backward does.)  A graph that is replayed
+ * beside other calls needs a workspace of its own.
+ *
+ * The gate's ids are those of the whole router row.  A rank that holds experts
+ * first .. first + n - 1 sorts ids - first with E = n: ids below 0 or from n
+ * on belong to other ranks.
  * ------------------------------------------------------------------------ */
 
 #define LRMOE_MAX_GATE_EXPERTS 1024 /* experts of a router row               */
@@ -530,8 +536,8 @@ lrmoe_status lrmoe_route_sort(int64_t T, int32_t K, int32_t E, const int32_t* id
 
 /* xp[pos[t, k]] = x[t]: x [T, D], xp [P, D] of one type.  P is the capacity
  * of xp: a place outside 0..P-1 is skipped, and rows no slot names are left
- * as they were.  (lrmoe_grouped_forward can read x through row_index
- * instead, without this copy.) */
+ * as they were.  Two slots must not share a place.  (lrmoe_grouped_forward
+ * can read x through row_index instead, without this copy.) */
 lrmoe_status lrmoe_dispatch(int32_t dtype, int64_t T, int32_t K, int32_t D, int64_t P,
                             const void* x, const int32_t* pos, void* xp, void* stream);
 

@@ -25,7 +25,12 @@
 //   few rows       one workgroup's walk over K: 2048 values take 7 to 9 us for 1
 //                  to 16 rows
 //   float32        the float32 matrix rate (157 TFLOP/s): 4097 pairs, 768 -> 2048
-//                  124 us, 104 TFLOP/s
+//                  124 us, 104 TFLOP/s; few rows read W: 32 pairs over 201 MB of
+//                  W 45 us, 4.5 TB/s
+//   more capacity than pairs
+//                  empty workgroups, and a variant for the capacity: 512 pairs,
+//                  2048 -> 1536 SwiGLU 19.7 us at their own size, 21.1 at eight
+//                  times that; 32768 pairs 218 and 228 us, 768 -> 2048 131 and 159
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -834,6 +839,8 @@ hipError_t forward_bf16(const ForwardArgs& a, int F, bool far, hipStream_t s) {
   typedef uint16_t T;
   constexpr int h = GLU ? 2 : 1;   // W rows of an output column
   if (expected(a, F, 16, 32 / h) <= 320) return launch_few_rows<T, 2, GLU>(a, F, s);
+  // 64-bit addresses, one shape: the 32768 pairs of a 2048 -> 1536 SwiGLU take 192
+  // us from an x just within a buffer's reach and 294 us from one beyond it
   if (far) return launch_gemm<Gemm<T, 32, 64, 2, 2, 3, GLU, true>>(a, F, s);
   // few rows for much W: wide tiles keep more of W in flight (16 experts of
   // 4096 columns and 2816 rows, 8 rows each: 67 us, 76 with the tiles below)

@@ -17,7 +17,11 @@
 // order.  They are bound by memory traffic; a copy on this card moves 5.1 TB/s
 // (32768 tokens, 8 slots, rows of 2048 bf16: dispatch 231 us, 5.2 TB/s; combine
 // onto a residual 258 us, 5.2 TB/s; its gradient, 8191 tokens with rows of
-// 4096, 225 us, 5.1 TB/s).  A position outside 0..P-1 is skipped.
+// 4096, 225 us, 5.1 TB/s).  Narrow rows leave lanes idle: at 64 columns (32768
+// tokens, 8 slots) dispatch and combine run at 2.1 and 1.9 TB/s, from 256 columns
+// on at a copy's rate; combine's gradient, which gives a token a whole workgroup,
+// at 1.7 TB/s with 256 columns, 2.6 with 512, 4.4 with 1024.  A position outside
+// 0..P-1 is skipped.
 #include "forward.h"
 
 namespace lrmoe {
@@ -32,8 +36,10 @@ namespace {
 // expert by ballots over the bits of the id.  Bin E holds the pairs of other
 // ranks.  Up to kOneBlock ids the one workgroup does it all in one launch
 // (64 tokens, 8 slots: 4.2 us); more take a histogram launch first (262144 ids
-// over 128 experts 12.6 us, of which the two launches are 5 and 8; 655360 ids 24
-// us; with 8192 ids a workgroup instead of 2048 20.5 and 27 us).
+// over 128 experts 12.6 us, of which the two launches are 5 and 8; 655360 ids 23
+// us; with 8192 ids a workgroup instead of 2048 20.5 and 27 us).  Each workgroup
+// reads the histograms of all, so past that their number squared counts: 2.4
+// million ids take 68 us over 128 experts and 96 us over 256.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kOneBlock = 4096;   // ids of a call that one workgroup sorts
