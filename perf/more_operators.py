@@ -214,7 +214,7 @@ def prepare(case, seed):
     if c["gate"] == "channel":
         s["gate"] = (0.5 + _normal(g, (D,), torch.float32, 0.1)).to(dt)
     elif c["gate"] == "token":
-        s["gate"] = torch.rand((T,), generator=g, device=DEV)
+        s["gate"] = torch.rand((T, 1), generator=g, device=DEV)
     if op == "norm_grad":
         # what the forward pass has stored
         s["s"] = _norm(s)["s"] if c["branch"] else s["x"]
@@ -229,15 +229,15 @@ def _own(s):
     from pruned_expert_backward_amd import lrmoe as L
     c, op = s["case"], s["case"]["op"]
     if op == "quant_rows":
-        return L.fp8_quantize(s["x"])
+        return L.quantize_rows(s["x"])
     if op == "quant_weights":
-        return L.fp8_quantize_weights(s["W"], transpose=c["transpose"])
+        return L.quantize_weights(s["W"], transpose=c["transpose"])
     if op == "product":
         act = {"none": L.ACT_NONE, "relu": L.ACT_RELU, "silu": L.ACT_SILU, "gelu": L.ACT_GELU,
                "swiglu": L.ACT_SWIGLU}[c["act"]]
-        return L.grouped_forward_fp8(s["seg"], L.fp8_quantize(s["x"]), s["W"],
-                                     row_index=s["row"], bias=s["bias"], residual=s["res"],
-                                     act=act, save_pre=c["pre"])
+        return L.grouped_forward_quantized(s["seg"], L.quantize_rows(s["x"]), s["W"],
+                                           row_index=s["row"], bias=s["bias"],
+                                           residual=s["res"], act=act, save_pre=c["pre"])
     if op == "norm":
         return L.residual_norm(s["x"], y=s["y"], weight=s["w"], branch_weight=s["wb"],
                                gate=s["gate"], scale=c["scale"])
@@ -373,11 +373,6 @@ def _rstd(x):
     return 1 / torch.sqrt((x * x).mean(1, keepdim=True) + NORM_EPS)
 
 
-def _gate_of(s):
-    gate = s["gate"].float()
-    return gate[:, None] if s["case"]["gate"] == "token" else gate
-
-
 def _norm(s):
     c, out = s["case"], {}
     x = s["x"].float()
@@ -385,7 +380,7 @@ def _norm(s):
         n = s["y"].float()
         if s["wb"] is not None:
             n = n * _rstd(n) * s["wb"].float()
-        x = c["scale"] * x + (n if s["gate"] is None else _gate_of(s) * n)
+        x = c["scale"] * x + (n if s["gate"] is None else s["gate"].float() * n)
         out["s"] = x.to(s["x"].dtype)
     if s["w"] is not None:
         out["h"] = (x * _rstd(x) * s["w"].float()).to(s["x"].dtype)
@@ -410,10 +405,10 @@ def _norm_grad(s):
     if s["wb"] is not None:
         r, w = _rstd(n), s["wb"].float()
         n = n * r
-    dn = d if s["gate"] is None else _gate_of(s) * d
+    dn = d if s["gate"] is None else s["gate"].float() * d
     if s["gate"] is not None:
         dg = d * n if w is None else d * n * w
-        out["dgate"] = (dg.sum(1) if c["gate"] == "token"
+        out["dgate"] = (dg.sum(1, keepdim=True) if c["gate"] == "token"
                         else dg.sum(0, dtype=torch.float64).float())
     if w is not None:
         out["dbranch_weight"] = (dn * n).sum(0, dtype=torch.float64).float()
@@ -602,7 +597,7 @@ def _exact_rms(x, w):
 def _exact_stream(s, x, y, wb, gate):
     n = y if wb is None else _exact_rms(y, wb)
     if gate is not None:
-        n = n * (gate[:, None] if s["case"]["gate"] == "token" else gate)
+        n = n * gate
     return s["case"]["scale"] * x + n
 
 
