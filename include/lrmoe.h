@@ -64,7 +64,7 @@
 extern "C" {
 #endif
 
-#define LRMOE_ABI_VERSION 5
+#define LRMOE_ABI_VERSION 6
 #define LRMOE_MAX_EXPERTS 256
 
 typedef enum {
@@ -622,6 +622,153 @@ lrmoe_status lrmoe_act_backward(const lrmoe_forward* fw, int32_t dz_dtype,
                                 const int32_t* seg_offsets, const void* dy, const void* pre_a,
                                 const void* pre_b, void* dz, float* dbias, void* workspace,
                                 size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit expert products.  Values in e4m3 (finite up to 448), one power-of-two
+ * scale 2^(byte - 127) for each block of 128: the smallest one with the block's
+ * largest magnitude at most 448 * scale (1 for a block of zeros).  Rows have blocks
+ * of 1 x 128, weights of 128 x 128; the last block of a row, column or weight may
+ * be smaller.  A row of scales has ceil(columns / 128) bytes, padded with 127
+ * to a multiple of four:
+ *   S(d) = 4 * ceil(ceil(d / 128) / 4)
+ * Infinity and NaN become the NaN code and do not count in their block's scale.
+ * Rows in 8 bits are whole 16-byte pieces: their lengths are multiples of 16.
+ *
+ * Gradients: dx of a product is the product of the quantised dz with the
+ * transposed weights (qt, scale_t), through lrmoe_grouped_forward_quantized; dW is
+ * lrmoe_grouped_backward on the unrounded rows.
+ * ------------------------------------------------------------------------ */
+
+/* Rows to 8 bits: x [T, D] of type dtype, q uint8 (e4m3) [T, D], scale uint8
+ * [T, S(D)].  0 <= T < 2^31, D a multiple of 16. */
+lrmoe_status lrmoe_quantize_rows(int32_t dtype, int64_t T, int32_t D, const void* x, uint8_t* q,
+                                uint8_t* scale, void* stream);
+
+/* Weights to 8 bits: W [E, d_out, d_in] of type dtype, q uint8 [E, d_out, d_in],
+ * scale uint8 [E, ceil(d_out / 128), S(d_in)]; and, unless qt and scale_t are NULL
+ * (both or neither), the same values and scales transposed: qt [E, d_in, d_out],
+ * scale_t [E, ceil(d_in / 128), S(d_out)].  d_in a multiple of 16, d_out of 8
+ * (with qt: of 16). */
+lrmoe_status lrmoe_quantize_weights(int32_t dtype, int32_t E, int32_t d_out, int32_t d_in,
+                                        const void* W, uint8_t* q, uint8_t* scale, uint8_t* qt,
+                                        uint8_t* scale_t, void* stream);
+
+/* lrmoe_grouped_forward with x and W in 8 bits: xq [T, d_in], x_scale [T, S(d_in)], Wq
+ * [E, d_out, d_in], W_scale [E, ceil(d_out / 128), S(d_in)].  Everything else is as
+ * there; fw->dtype, the type of bias, residual, y, pre_a and pre_b, is LRMOE_BF16
+ * (else LRMOE_ERR_DTYPE), and d_in a multiple of 16.  float32 accumulation and
+ * epilogue, one rounding. */
+lrmoe_status lrmoe_grouped_forward_quantized(const lrmoe_forward* fw, const int32_t* seg_offsets,
+                                       const int32_t* row_index, const uint8_t* xq,
+                                       const uint8_t* x_scale, const uint8_t* Wq,
+                                       const uint8_t* W_scale, const void* bias,
+                                       const void* residual, void* y, void* pre_a, void* pre_b,
+                                       void* stream);
+
+/* ------------------------------------------------------------------------
+ * The norms around a block, with its gate and residual scale:
+ *   b_t = y_t                              without branch_weight
+ *         y_t * rms(y_t) * branch_weight   with it;  rms(v) = (mean(v^2) + eps)^-1/2
+ *   s_t = scale * x_t + gate * b_t
+ *   h_t = s_t * rms(s_t) * weight
+ * s is the residual stream behind the block whose output is y, h the next
+ * block's input.  float32 sums and statistics; h is computed from s before its
+ * rounding; each output is rounded once.
+ * ------------------------------------------------------------------------ */
+
+#define LRMOE_MAX_NORM_WIDTH 16384 /* columns of a row */
+
+typedef enum {
+  LRMOE_BRANCH_GATE_NONE = 0,    /* 1                                        */
+  LRMOE_BRANCH_GATE_CHANNEL = 1, /* one factor a column, [D] of type dtype   */
+  LRMOE_BRANCH_GATE_TOKEN = 2    /* one factor a row, float32 [T]            */
+} lrmoe_branch_gate;
+
+typedef struct {
+  int64_t T;      /* rows, 0 <= T < 2^31                                     */
+  int32_t D;      /* columns, at most LRMOE_MAX_NORM_WIDTH, whole 16 bytes   */
+  int32_t dtype;  /* of x, y, s, h, their gradients and the weights          */
+  int32_t gate;   /* lrmoe_branch_gate                                       */
+  float scale;    /* factor of the residual                                  */
+  float eps;      /* at least 0                                              */
+} lrmoe_norm;
+
+/* x, y, s, h [T, D]; branch_weight, weight [D].  y NULL: no branch; then
+ * branch_weight, gate and s have to be NULL, scale 1 (else LRMOE_ERR_INVALID), and
+ * s_t is x_t.  weight and h go together (both or neither: LRMOE_ERR_NULL), and so do
+ * gate and its kind; with y, s is needed. */
+lrmoe_status lrmoe_residual_norm(const lrmoe_norm* nm, const void* x, const void* y,
+                                 const void* branch_weight, const void* gate, const void* weight,
+                                 void* s, void* h, void* stream);
+
+/* Workspace bytes of lrmoe_residual_norm_backward. */
+lrmoe_status lrmoe_residual_norm_backward_workspace(const lrmoe_norm* nm, size_t* bytes_out);
+
+/* Gradient, at the stored s (x itself without a branch; not read without weight) and
+ * y, from ds [T, D] (NULL: nothing arrives at s but through h) and dh [T, D] (with
+ * weight and only then):
+ *   dx [T, D], dy [T, D] (with y and only then)
+ *   dweight, dbranch_weight float32 [D] (with the weights) or NULL: not computed
+ *   dgate float32 [D] or [T] (with the gate) or NULL: not computed
+ * Sums over rows do not depend on timing.  workspace: not read when only dx, dy and
+ * a token's dgate are asked for (then NULL will do). */
+lrmoe_status lrmoe_residual_norm_backward(const lrmoe_norm* nm, const void* ds, const void* dh,
+                                          const void* s, const void* y, const void* branch_weight,
+                                          const void* gate, const void* weight, void* dx, void* dy,
+                                          float* dweight, float* dbranch_weight, float* dgate,
+                                          void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * AdamW over many tensors in one call (one launch for each 48 tensors of the
+ * same types), in place:
+ *   g' = grad_scale * g
+ *   m  = beta1 m + (1 - beta1) g'         v = beta2 v + (1 - beta2) g'^2
+ *   p  = (1 - lr * weight_decay) p
+ *        - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in float32.  The states are float32 [n], or 8-bit: e4m3 [n] with a scale byte
+ * for each run of 128 elements (the blocks of the products above), m itself and,
+ * in v's place, sqrt(v).  p is updated from the unrounded m and v.  8-bit states
+ * and bfloat16 parameters are rounded stochastically: up with a probability of
+ * the distance from the lower neighbour (in 65536ths), so that small changes are
+ * not lost on average; a second moment that is not zero is not rounded to zero.
+ * The random bits of element i of tensor k are a hash of (seed, step, k, i):
+ *   mix(a): a ^= a >> 16; a *= 0x6A09E667; a ^= a >> 15; a *= 0xBB67AE85;
+ *           a ^= a >> 16                                        (32 bits)
+ *   key = mix(mix(seed + step * 0x9E3779B9) + (k + 1) * 0x3C6EF373)
+ *   r   = mix((i mod 2^32) + key)
+ * r's upper half rounds m, its lower half sqrt(v), the upper half of
+ * mix(r + 0xA54FF53B) a bfloat16 p.
+ * ------------------------------------------------------------------------ */
+
+typedef struct {
+  int64_t n;         /* elements (0: skipped)                                */
+  void* p;           /* parameter [n], updated                               */
+  const void* g;     /* gradient [n]                                         */
+  void* m;           /* first moment [n], updated                            */
+  void* v;           /* second moment (8-bit: its root) [n], updated         */
+  uint8_t* m_scale;  /* 8-bit states: [ceil(n / 128)], updated; else NULL    */
+  uint8_t* v_scale;  /* with m_scale, both or neither                        */
+  void* copy;        /* bfloat16 [n] or NULL: p rounded to nearest; p float32 */
+  int32_t p_dtype;   /* lrmoe_dtype of p                                     */
+  int32_t g_dtype;   /* lrmoe_dtype of g                                     */
+} lrmoe_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay; /* 0 <= beta < 1, the others >= 0 */
+  int64_t step;            /* from 1 on                                      */
+  uint32_t seed;           /* of the stochastic rounding                     */
+  const float* lr_at;      /* device float32 or NULL: in lr's place          */
+  const int64_t* step_at;  /* device int64 or NULL: in step's place (from 1 on) */
+  const float* grad_scale; /* device float32 or NULL (1)                     */
+  const float* skip;       /* device float32 or NULL: nothing is changed if not 0 */
+} lrmoe_adamw;
+
+/* tensors: host array of count descriptors (read before the call returns), k their
+ * index in it; device pointers 16-byte aligned except the four scalars (their own
+ * size).  A captured call replays with the descriptors and host scalars of its
+ * capture: lr_at and step_at are for that.  No two buffers may overlap. */
+lrmoe_status lrmoe_adamw_step(const lrmoe_adamw* cfg, const lrmoe_adamw_tensor* tensors,
+                              int32_t count, void* stream);
 
 #ifdef __cplusplus
 }

@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblrmoe.so")
 SOURCES = ["api.cpp", "score_select.hip", "gather.hip", "grouped_gemm.hip", "plan_quota.hip",
-           "api_forward.cpp", "gate.hip", "route.hip", "grouped_forward.hip", "act_backward.hip"]
+           "api_forward.cpp", "gate.hip", "route.hip", "grouped_forward.hip", "act_backward.hip",
+           "api_block.cpp", "quantize.hip", "grouped_fp8.hip", "block_norm.hip", "adamw.hip"]
 ARCH = "gfx950"
 
 

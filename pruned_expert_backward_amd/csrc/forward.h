@@ -134,4 +134,36 @@ hipError_t launch_act_backward(int dtype, int out_dtype, int act, const int32_t*
                                const void* dy, const void* a, const void* b, int64_t P, int32_t E,
                                int32_t F, void* dz, float* dbias, float* ws, hipStream_t s);
 
+// ---- 8-bit blocks (fp8.h), the norms around a block, the optimizer's step
+hipError_t launch_fp8_quantize(int dtype, const void* x, int64_t rows, int32_t D, uint8_t* q,
+                               uint8_t* scale, hipStream_t s);
+// qt and scale_t may be null
+hipError_t launch_fp8_quantize_weights(int dtype, const void* W, int32_t E, int32_t N, int32_t K,
+                                       uint8_t* q, uint8_t* scale, uint8_t* qt, uint8_t* scale_t,
+                                       hipStream_t s);
+// a.x and a.W in e4m3, everything else bfloat16
+hipError_t launch_grouped_forward_fp8(const ForwardArgs& a, const uint8_t* x_scale,
+                                      const uint8_t* W_scale, hipStream_t s);
+
+struct NormArgs {
+  const void* x;               // [T, D]; the gradient: s, as the forward has stored it
+  const void* y;               // [T, D] or null: no branch
+  const void* branch_weight;   // [D] or null
+  const void* gate;            // [D], float32 [T], or null
+  const void* weight;          // [D] or null
+  int64_t T;
+  int32_t D, gate_kind;
+  float scale, eps;
+};
+hipError_t launch_residual_norm(int dtype, const NormArgs& a, void* s, void* h, hipStream_t st);
+size_t residual_norm_workspace(int64_t T, int32_t D);
+// the sums over rows (dweight, dbranch_weight, dgate of a channel) may be null
+hipError_t launch_residual_norm_backward(int dtype, const NormArgs& a, const void* ds,
+                                         const void* dh, void* dx, void* dy, float* dweight,
+                                         float* dbranch_weight, float* dgate, float* ws,
+                                         hipStream_t st);
+
+hipError_t launch_adamw(const lrmoe_adamw* c, const lrmoe_adamw_tensor* t, int32_t count,
+                        hipStream_t s);
+
 }  // namespace lrmoe

@@ -23,10 +23,14 @@ SCORE_LRM, SCORE_GRAD_SQNORM, SCORE_GRAD_L1 = 0, 1, 2
 QUOTA_RATIO, QUOTA_BUDGET = 0, 1
 GATE_SOFTMAX, GATE_SIGMOID = 0, 1
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_SWIGLU = 0, 1, 2, 3, 4
+BRANCH_GATE_NONE, BRANCH_GATE_CHANNEL, BRANCH_GATE_TOKEN = 0, 1, 2
 MAX_EXPERTS = 256
 MAX_GATE_EXPERTS = 1024
 MAX_TOPK = 64
-ABI_VERSION = 5
+MAX_NORM_WIDTH = 16384
+FP8 = torch.float8_e4m3fn
+FP8_BLOCK = 128   # values that share a scale
+ABI_VERSION = 6
 
 STATUS = {0: "LRMOE_OK", 1: "LRMOE_ERR_NULL", 2: "LRMOE_ERR_INVALID", 3: "LRMOE_ERR_SHAPE",
           4: "LRMOE_ERR_ALIGN", 5: "LRMOE_ERR_DTYPE", 6: "LRMOE_ERR_WORKSPACE",
@@ -44,7 +48,10 @@ EXPORTS = ["lrmoe_abi_version", "lrmoe_status_string", "lrmoe_plan_quota",
            "lrmoe_gate_topk", "lrmoe_gate_topk_backward", "lrmoe_route_sort_workspace",
            "lrmoe_route_sort", "lrmoe_dispatch", "lrmoe_dispatch_backward", "lrmoe_combine",
            "lrmoe_combine_backward", "lrmoe_grouped_forward", "lrmoe_act_backward_workspace",
-           "lrmoe_act_backward"]
+           "lrmoe_act_backward", "lrmoe_quantize_rows", "lrmoe_quantize_weights",
+           "lrmoe_grouped_forward_quantized", "lrmoe_residual_norm",
+           "lrmoe_residual_norm_backward_workspace", "lrmoe_residual_norm_backward",
+           "lrmoe_adamw_step"]
 TIMING_SLOTS = 8
 
 
@@ -78,6 +85,24 @@ class Gate(C.Structure):
 class Forward(C.Structure):
     _fields_ = [("E", C.c_int32), ("dtype", C.c_int32), ("P", C.c_int64), ("T", C.c_int64),
                 ("d_out", C.c_int32), ("d_in", C.c_int32), ("act", C.c_int32)]
+
+
+class Norm(C.Structure):
+    _fields_ = [("T", C.c_int64), ("D", C.c_int32), ("dtype", C.c_int32), ("gate", C.c_int32),
+                ("scale", C.c_float), ("eps", C.c_float)]
+
+
+class AdamWTensor(C.Structure):
+    _fields_ = [("n", C.c_int64), ("p", C.c_void_p), ("g", C.c_void_p), ("m", C.c_void_p),
+                ("v", C.c_void_p), ("m_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("copy", C.c_void_p), ("p_dtype", C.c_int32), ("g_dtype", C.c_int32)]
+
+
+class AdamW(C.Structure):
+    _fields_ = [("lr", C.c_double), ("beta1", C.c_double), ("beta2", C.c_double),
+                ("eps", C.c_double), ("weight_decay", C.c_double), ("step", C.c_int64),
+                ("seed", C.c_uint32), ("lr_at", C.c_void_p), ("step_at", C.c_void_p),
+                ("grad_scale", C.c_void_p), ("skip", C.c_void_p)]
 
 
 _lib_handle = None
@@ -161,7 +186,14 @@ def lib() -> C.CDLL:
             ("lrmoe_combine_backward", [i32, i64, i32, i32, i64] + [_P] * 7),
             ("lrmoe_grouped_forward", [C.POINTER(Forward)] + [_P] * 10),
             ("lrmoe_act_backward_workspace", [C.POINTER(Forward), C.POINTER(C.c_size_t)]),
-            ("lrmoe_act_backward", [C.POINTER(Forward), i32] + [_P] * 7 + [C.c_size_t, _P])):
+            ("lrmoe_act_backward", [C.POINTER(Forward), i32] + [_P] * 7 + [C.c_size_t, _P]),
+            ("lrmoe_quantize_rows", [i32, i64, i32] + [_P] * 4),
+            ("lrmoe_quantize_weights", [i32] * 4 + [_P] * 6),
+            ("lrmoe_grouped_forward_quantized", [C.POINTER(Forward)] + [_P] * 12),
+            ("lrmoe_residual_norm", [C.POINTER(Norm)] + [_P] * 8),
+            ("lrmoe_residual_norm_backward_workspace", [C.POINTER(Norm), C.POINTER(C.c_size_t)]),
+            ("lrmoe_residual_norm_backward", [C.POINTER(Norm)] + [_P] * 13 + [C.c_size_t, _P]),
+            ("lrmoe_adamw_step", [C.POINTER(AdamW), C.POINTER(AdamWTensor), i32, _P])):
         fn = getattr(L, name)
         fn.restype, fn.argtypes = C.c_int, args
     _lib_handle = L
@@ -947,3 +979,285 @@ def act_backward(seg_offsets, dy, pre_a=None, pre_b=None, act: int = ACT_NONE,
           o("dz", dz, dz.dtype, (P, d_out), dev),
           None if db is None else o("dbias", db, torch.float32, (E, d_out), dev), addr, n)
     return out
+
+
+# ------------------------------------------------- 8-bit products, norms, optimizer
+# e4m3 values with a power-of-two scale for each block of 128 (as the exponent
+# byte e + 127); the norms around a block; the optimizer's step.
+
+def scale_row_bytes(d: int) -> int:
+    """Bytes of a row of scales over d columns."""
+    return (-(-d // FP8_BLOCK) + 3) // 4 * 4
+
+
+def _opt(name: str, t: Optional[torch.Tensor], dtype, shape, dev):
+    return None if t is None else _arg(name, t, dtype, shape, dev)
+
+
+def quantize_rows(x, out: Optional[dict] = None) -> dict:
+    """Rows x [T, D] to 8 bits: q float8_e4m3fn [T, D] and scale uint8
+    [T, scale_row_bytes(D)], one for each block of 1 x 128."""
+    dev = _device(x)
+    _rank("x", x, 2)
+    T, D = x.shape
+    S = scale_row_bytes(D)
+    o = _fresh if out is None else _arg
+    if out is None:
+        out = dict(q=torch.empty(T, D, dtype=FP8, device=dev),
+                   scale=torch.empty(T, S, dtype=torch.uint8, device=dev))
+    _call("lrmoe_quantize_rows", dev, storage_dtype(x.dtype), T, D,
+          _arg("x", x, x.dtype, (T, D), dev), o("q", out["q"], FP8, (T, D), dev),
+          o("scale", out["scale"], torch.uint8, (T, S), dev))
+    return out
+
+
+def quantize_weights(W, transpose: bool = False, out: Optional[dict] = None) -> dict:
+    """Weights W [E, d_out, d_in] to 8 bits with a scale for each block of 128 x 128:
+    q [E, d_out, d_in], scale uint8 [E, ceil(d_out / 128), scale_row_bytes(d_in)] and,
+    with transpose (or where out holds them), the same values transposed: qt [E, d_in, d_out],
+    scale_t [E, ceil(d_in / 128), scale_row_bytes(d_out)]."""
+    dev = _device(W)
+    _rank("W", W, 3)
+    E, N, K = W.shape
+    sn, sk = (E, -(-N // FP8_BLOCK), scale_row_bytes(K)), (E, -(-K // FP8_BLOCK), scale_row_bytes(N))
+    u8, o = torch.uint8, _fresh if out is None else _arg
+    if out is None:
+        out = dict(q=torch.empty(E, N, K, dtype=FP8, device=dev),
+                   scale=torch.empty(sn, dtype=u8, device=dev))
+        if transpose:
+            out["qt"] = torch.empty(E, K, N, dtype=FP8, device=dev)
+            out["scale_t"] = torch.empty(sk, dtype=u8, device=dev)
+    elif transpose:
+        _asked("transpose", out, "qt", "scale_t")
+    qt, st = out.get("qt"), out.get("scale_t")
+    _call("lrmoe_quantize_weights", dev, storage_dtype(W.dtype), E, N, K,
+          _arg("W", W, W.dtype, (E, N, K), dev), o("q", out["q"], FP8, (E, N, K), dev),
+          o("scale", out["scale"], u8, sn, dev),
+          None if qt is None else o("qt", qt, FP8, (E, K, N), dev),
+          None if st is None else o("scale_t", st, u8, sk, dev))
+    return out
+
+
+def transposed_weights(W: dict) -> dict:
+    """The transposed weights of quantize_weights(..., transpose=True), as
+    grouped_forward_quantized takes them."""
+    return dict(q=W["qt"], scale=W["scale_t"])
+
+
+def grouped_forward_quantized(seg_offsets, x: dict, W: dict, row_index=None, bias=None, residual=None,
+                        act: int = ACT_NONE, save_pre: bool = False,
+                        out: Optional[dict] = None) -> dict:
+    """grouped_forward with x (q [T, d_in] and scale) and W (q [E, d_out, d_in] and
+    scale) as quantize_rows and quantize_weights give them.  bias, residual, y and
+    the pre-activations are bfloat16.  The input's gradient is the same call on the
+    quantised output gradient with transposed_weights(W)."""
+    xq, xs, Wq, Ws = x["q"], x["scale"], W["q"], W["scale"]
+    dev = _device(xq)
+    _rank("x", xq, 2)
+    _rank("W", Wq, 3)
+    T, d_in = xq.shape
+    E, d_out, dt, u8 = Wq.shape[0], Wq.shape[1], torch.bfloat16, torch.uint8
+    P = T if row_index is None else row_index.numel()
+    glu = act == ACT_SWIGLU
+    F = d_out // 2 if glu else d_out
+    S = scale_row_bytes(d_in)
+    o = _fresh if out is None else _arg
+    if out is None:
+        out = dict(y=torch.empty(P, F, dtype=dt, device=dev))
+        if save_pre:
+            out["pre_a"] = torch.empty(P, F, dtype=dt, device=dev)
+            if glu:
+                out["pre_b"] = torch.empty(P, F, dtype=dt, device=dev)
+    elif save_pre:
+        _asked("save_pre", out, *(("pre_a", "pre_b") if glu else ("pre_a",)))
+    fw = Forward(E, BF16, P, T, d_out, d_in, int(act))
+    pa, pb = out.get("pre_a"), out.get("pre_b")
+    _call("lrmoe_grouped_forward_quantized", dev, C.byref(fw),
+          _arg("seg_offsets", seg_offsets, torch.int32, (E + 1,), dev),
+          _opt("row_index", row_index, torch.int32, (P,), dev),
+          _arg("x", xq, FP8, (T, d_in), dev), _arg("x scale", xs, u8, (T, S), dev),
+          _arg("W", Wq, FP8, (E, d_out, d_in), dev),
+          _arg("W scale", Ws, u8, (E, -(-d_out // FP8_BLOCK), S), dev),
+          _opt("bias", bias, dt, (E, d_out), dev), _opt("residual", residual, dt, (P, F), dev),
+          o("y", out["y"], dt, (P, F), dev),
+          None if pa is None else o("pre_a", pa, dt, (P, F), dev),
+          None if pb is None else o("pre_b", pb, dt, (P, F), dev))
+    return out
+
+
+def _branch_gate(gate, y, T: int, D: int, dt, dev):
+    """(kind, address, shape) of a branch's gate: [D] in the rows' type, or float32 [T, 1]."""
+    if gate is None:
+        return BRANCH_GATE_NONE, None, None
+    if y is None:
+        raise ValueError("gate: there is no branch")
+    if gate.dim() == 2:
+        return BRANCH_GATE_TOKEN, _arg("gate", gate, torch.float32, (T, 1), dev), (T, 1)
+    return BRANCH_GATE_CHANNEL, _arg("gate", gate, dt, (D,), dev), (D,)
+
+
+def residual_norm(x, y=None, weight=None, branch_weight=None, gate=None, scale: float = 1.0,
+                  eps: float = 1e-6, out: Optional[dict] = None) -> dict:
+    """The end of a block and the next one's norm, rows [T, D] of x's type:
+    s = scale * x + gate * y * rms(y) * branch_weight (no norm of y without
+    branch_weight) and, with weight, h = s * rms(s) * weight, where rms(v) =
+    (mean(v^2) + eps)^-1/2.  gate is [D] (x's type) or float32 [T, 1].  Without y
+    only h, the norm of x, is computed."""
+    dev = _device(x)
+    _rank("x", x, 2)
+    T, D = x.shape
+    dt = x.dtype
+    if y is None and (branch_weight is not None or scale != 1.0):
+        raise ValueError("branch_weight and scale: there is no branch")
+    if y is None and weight is None:
+        raise ValueError("neither y nor weight: nothing to compute")
+    kind, gate_at, _ = _branch_gate(gate, y, T, D, dt, dev)
+    o = _fresh if out is None else _arg
+    if out is None:
+        out = {}
+        if y is not None:
+            out["s"] = torch.empty(T, D, dtype=dt, device=dev)
+        if weight is not None:
+            out["h"] = torch.empty(T, D, dtype=dt, device=dev)
+    nm = Norm(T, D, storage_dtype(dt), kind, float(scale), float(eps))
+    _call("lrmoe_residual_norm", dev, C.byref(nm), _arg("x", x, dt, (T, D), dev),
+          _opt("y", y, dt, (T, D), dev), _opt("branch_weight", branch_weight, dt, (D,), dev),
+          gate_at, _opt("weight", weight, dt, (D,), dev),
+          None if y is None else o("s", out["s"], dt, (T, D), dev),
+          None if weight is None else o("h", out["h"], dt, (T, D), dev))
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def residual_norm_backward_workspace_bytes(T: int, D: int, dtype: int) -> int:
+    n, nm = C.c_size_t(0), Norm(T, D, dtype, BRANCH_GATE_NONE, 1.0, 0.0)
+    check("lrmoe_residual_norm_backward_workspace",
+          lib().lrmoe_residual_norm_backward_workspace(C.byref(nm), C.byref(n)))
+    return int(n.value)
+
+
+def residual_norm_backward(s, ds=None, dh=None, y=None, weight=None, branch_weight=None,
+                           gate=None, scale: float = 1.0, eps: float = 1e-6,
+                           out: Optional[dict] = None, ws=None) -> dict:
+    """Gradient of residual_norm at its output s (x itself without y) and y, from
+    ds (None: nothing arrives at s but through h) and dh: dx, with y dy, and float32
+    dweight [D], dbranch_weight [D] and dgate (the gate's shape) for those that are there;
+    where out is given, those of the last three are computed that it holds."""
+    dev = _device(s)
+    _rank("s", s, 2)
+    T, D = s.shape
+    dt, f32 = s.dtype, torch.float32
+    if y is None and (branch_weight is not None or scale != 1.0):
+        raise ValueError("branch_weight and scale: there is no branch")
+    if (weight is None) != (dh is None):
+        raise ValueError("weight and dh go together")
+    if ds is None and dh is None:
+        raise ValueError("neither ds nor dh: no gradient arrives")
+    kind, gate_at, gate_shape = _branch_gate(gate, y, T, D, dt, dev)
+    o = _fresh if out is None else _arg
+    if out is None:
+        out = dict(dx=torch.empty(T, D, dtype=dt, device=dev))
+        if y is not None:
+            out["dy"] = torch.empty(T, D, dtype=dt, device=dev)
+        if weight is not None:
+            out["dweight"] = torch.empty(D, dtype=f32, device=dev)
+        if branch_weight is not None:
+            out["dbranch_weight"] = torch.empty(D, dtype=f32, device=dev)
+        if gate is not None:
+            out["dgate"] = torch.empty(gate_shape, dtype=f32, device=dev)
+    dw, dwb, dg = (out.get(k) for k in ("dweight", "dbranch_weight", "dgate"))
+    for name, d, given in (("dweight", dw, weight), ("dbranch_weight", dwb, branch_weight),
+                           ("dgate", dg, gate)):
+        if d is not None and given is None:
+            raise ValueError(f"{name}: out holds a gradient of what is not there")
+    nm = Norm(T, D, storage_dtype(dt), kind, float(scale), float(eps))
+    sums = dw is not None or dwb is not None or (dg is not None and kind == BRANCH_GATE_CHANNEL)
+    need = residual_norm_backward_workspace_bytes(T, D, storage_dtype(dt)) if sums else 0
+    addr, n, _keep = _workspace(need, ws, dev)
+    _call("lrmoe_residual_norm_backward", dev, C.byref(nm), _opt("ds", ds, dt, (T, D), dev),
+          _opt("dh", dh, dt, (T, D), dev), _arg("s", s, dt, (T, D), dev),
+          _opt("y", y, dt, (T, D), dev), _opt("branch_weight", branch_weight, dt, (D,), dev),
+          gate_at, _opt("weight", weight, dt, (D,), dev),
+          o("dx", out["dx"], dt, (T, D), dev),
+          None if y is None else o("dy", out["dy"], dt, (T, D), dev),
+          None if dw is None else o("dweight", dw, f32, (D,), dev),
+          None if dwb is None else o("dbranch_weight", dwb, f32, (D,), dev),
+          None if dg is None else o("dgate", dg, f32, gate_shape, dev), addr, n)
+    return out
+
+
+def adamw_state(param, bits: int = 32) -> dict:
+    """Zero moments of a parameter: float32 m and v, or 8-bit (float8_e4m3fn) m and
+    root (the root of the second moment) with m_scale and root_scale, uint8, a byte for each
+    run of 128 elements."""
+    n, dev = param.numel(), param.device
+    if bits == 32:
+        return dict(m=torch.zeros(n, dtype=torch.float32, device=dev),
+                    v=torch.zeros(n, dtype=torch.float32, device=dev))
+    if bits != 8:
+        raise ValueError(f"bits: 32 or 8 expected, got {bits}")
+    b = -(-n // FP8_BLOCK)
+    code = lambda: torch.zeros(n, dtype=torch.uint8, device=dev).view(FP8)  # noqa: E731
+    one = lambda: torch.full((b,), 127, dtype=torch.uint8, device=dev)      # noqa: E731
+    return dict(m=code(), m_scale=one(), root=code(), root_scale=one())
+
+
+def _scalar_at(name: str, t: Optional[torch.Tensor], dtype, dev):
+    """Address of a scalar on the device."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {dtype} expected, got {t.dtype}")
+    if t.numel() != 1:
+        raise ValueError(f"{name}: one element expected, got {t.numel()}")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, the other tensors are on {dev}")
+    return t.data_ptr()
+
+
+def adamw_step(params: Sequence, grads: Sequence, states: Sequence, step, lr,
+               betas: tuple = (0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+               copies: Optional[Sequence] = None, grad_scale=None, skip=None,
+               seed: int = 0) -> None:
+    """One AdamW step over many tensors, in place: params (float32 or bfloat16), grads (float32
+    or bfloat16) of the same shapes, states as adamw_state makes them (of either kind), copies
+    (bfloat16 or None each, for float32 params: the rounded result).  step (from 1 on)
+    and lr are numbers, or one-element device tensors (int64, float32) that a captured
+    call reads at each replay.  grad_scale (float32 tensor) multiplies the gradients;
+    nothing is changed where skip (float32 tensor) is not 0.  seed: of the stochastic
+    rounding of 8-bit states and bfloat16 parameters; the step enters by itself."""
+    count = len(params)
+    if len(grads) != count or len(states) != count or (copies is not None and
+                                                       len(copies) != count):
+        raise ValueError("params, grads, states and copies have different lengths")
+    if count == 0:
+        return
+    dev = _device(params[0])
+    f32, u8 = torch.float32, torch.uint8
+    table = (AdamWTensor * count)()
+    for k in range(count):
+        p, g, st, a = params[k], grads[k], states[k], table[k]
+        n, shape = p.numel(), p.shape
+        a.n = n
+        a.p_dtype, a.g_dtype = storage_dtype(p.dtype), storage_dtype(g.dtype)
+        a.p = _arg("params", p, p.dtype, shape, dev)
+        a.g = _arg("grads", g, g.dtype, shape, dev)
+        if "root" in st:
+            b = (-(-n // FP8_BLOCK),)
+            a.m = _arg("m", st["m"], FP8, (n,), dev)
+            a.v = _arg("root", st["root"], FP8, (n,), dev)
+            a.m_scale = _arg("m_scale", st["m_scale"], u8, b, dev)
+            a.v_scale = _arg("root_scale", st["root_scale"], u8, b, dev)
+        else:
+            a.m = _arg("m", st["m"], f32, (n,), dev)
+            a.v = _arg("v", st["v"], f32, (n,), dev)
+        if copies is not None and copies[k] is not None:
+            a.copy = _arg("copies", copies[k], torch.bfloat16, shape, dev)
+    on_dev = isinstance(step, torch.Tensor), isinstance(lr, torch.Tensor)
+    cfg = AdamW(0.0 if on_dev[1] else float(lr), float(betas[0]), float(betas[1]), float(eps),
+                float(weight_decay), 0 if on_dev[0] else int(step), int(seed) & 0xFFFFFFFF,
+                _scalar_at("lr", lr, f32, dev) if on_dev[1] else None,
+                _scalar_at("step", step, torch.int64, dev) if on_dev[0] else None,
+                _scalar_at("grad_scale", grad_scale, f32, dev),
+                _scalar_at("skip", skip, f32, dev))
+    _call("lrmoe_adamw_step", dev, C.byref(cfg), table, count)
