@@ -8,8 +8,9 @@
 // A K step is one block: 128 bytes of every row, a cache line and the depth of
 // one scaled matrix instruction (v_mfma_scale_f32_16x16x128_f8f6f4), which takes the
 // two scale bytes of its rows as operands and adds the scaled products to float32
-// accumulators.  So the scales cost no arithmetic; they wait in LDS, as dwords of four
-// steps, and are shifted by a byte a step.
+// accumulators.  So the scales cost no arithmetic.  They wait in LDS, for each step and
+// lane in one piece: a lane's row blocks are the bytes of a dword, which the
+// instruction picks from.
 //
 // The instruction adds the products of a run of 8 on one scale and cuts off what
 // lies below 2^-13 of the largest (measured); the runs' sums and the accumulator are
@@ -30,28 +31,57 @@ struct Fp8Args {
   const uint8_t* ws;   // [E, ceil(d_out / 128), pitch]
 };
 
-// 32 of a row's 128 values of a step: chunks g and g + 4 of 16 bytes in lane group
-// g, the same ones in both operands.
+// 32 of a row's 128 values of a step: two chunks of 16 bytes in each lane, the same
+// ones in both operands.
 struct Frag {
   vec4u lo, hi;
 };
 
+// c + 2^(x + y - 254) a b, with x in byte XA of sa and y in byte XB of sb.
+template <int XA, int XB>
 __device__ __forceinline__ f32x4 mfma(const Frag& a, const Frag& b, f32x4 c, uint32_t sa,
                                       uint32_t sb) {
   const i32x8 va = {(int)a.lo[0], (int)a.lo[1], (int)a.lo[2], (int)a.lo[3],
                     (int)a.hi[0], (int)a.hi[1], (int)a.hi[2], (int)a.hi[3]};
   const i32x8 vb = {(int)b.lo[0], (int)b.lo[1], (int)b.lo[2], (int)b.lo[3],
                     (int)b.hi[0], (int)b.hi[1], (int)b.hi[2], (int)b.hi[3]};
-  // e4m3 in both; the scales' low bytes
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, c, 0, 0, 0, (int)sa, 0, (int)sb);
+  // e4m3 in both
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, c, 0, 0, XA, (int)sa, XB,
+                                                          (int)sb);
 }
 
 __device__ __forceinline__ int scale_blocks(int d) { return (d + kFp8Block - 1) / kFp8Block; }
 
-// Each column tile of each expert starts its K loop this many groups of four K steps
-// after its neighbour's and goes round, so that they do not all read the same few
-// memory channels.
-constexpr int kStaggerGroups = 1;
+// Each column tile of each expert starts its K loop this many K steps after its
+// neighbour's and goes round, so that they do not all read the same few memory channels;
+// not with 256-row tiles, which share their rows of x in the L2.
+constexpr int kStagger = 3;
+
+// Byte q of four dwords into dword q, byte by byte (a 4 x 4 transpose).
+__device__ __forceinline__ void flip_bytes(uint32_t (&w)[4]) {
+  const uint32_t lo01 = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u);
+  const uint32_t hi01 = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
+  const uint32_t lo23 = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u);
+  const uint32_t hi23 = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+  w[0] = __builtin_amdgcn_perm(lo23, lo01, 0x05040100u);
+  w[1] = __builtin_amdgcn_perm(lo23, lo01, 0x07060302u);
+  w[2] = __builtin_amdgcn_perm(hi23, hi01, 0x05040100u);
+  w[3] = __builtin_amdgcn_perm(hi23, hi01, 0x07060302u);
+}
+
+// Eight consecutive columns a lane from two neighbouring 16 x 16 results, which hold
+// four a lane: lane group g then has columns 8 g .. 8 g + 7 of the 32.
+__device__ __forceinline__ void eight_columns(const f32x4& p, const f32x4& q, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // rows of lanes [p0 p1 q0 q1], [p2 p3 q2 q3], then [p0 p2 q0 q2], [p1 p3 q1 q3]
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(p[i]), __float_as_uint(q[i]),
+                                                    false, false);
+    const auto s = __builtin_amdgcn_permlane16_swap(r[0], r[1], false, false);
+    v[i] = __uint_as_float(s[0]);
+    v[4 + i] = __uint_as_float(s[1]);
+  }
+}
 
 template <int WR, int WC, int WM, int WN, int NS, bool GLU, bool FAR = false>
 struct Gemm8 {
@@ -60,32 +90,22 @@ struct Gemm8 {
   static constexpr int kMB = MB, kNB = NB;
   static constexpr int kWaves = WM * WN;
   static constexpr int kThreads = 64 * kWaves;
-  static constexpr int kWavesPerSimd = 2;
+  static constexpr int kWavesPerSimd = WR * WC > 64 * 128 ? 1 : 2;
   static constexpr int TM = WM * WR, TN = WN * WC;
   static constexpr int kOut = GLU ? TN / 2 : TN;
   static constexpr int kChunks = RB / 16;
   static constexpr int kStage = (TM + TN) * RB;
   static constexpr int kPwA = TM * RB / 1024 / kWaves, kPwB = TN * RB / 1024 / kWaves;
   static constexpr int kLoads = kPwA + kPwB;
-  typedef Epilogue<uint16_t, WR, WC, WM, WN, GLU> Epi;
-  static constexpr int kStages = NS * kStage > Epi::kLds ? NS * kStage : Epi::kLds;
-  // scales: K steps that LDS holds at a time; dwords of a row, one more so that 16
-  // rows fall on distinct banks
-  static constexpr int kScaleSteps = 32;
-  static constexpr int kScalePitch = kScaleSteps / 4 + 1;
-  static constexpr int kLds = kStages + (TM + TN) * kScalePitch * 4;
-  static constexpr int R = NB < 4 ? NB : 4;   // B fragments in registers
-  // The scales of a wave's columns: one for all of them, which start at a multiple of
-  // WC; the up rows of SwiGLU start at F plus that and may cross into the next 128
-  // anywhere, so a lane looks at its own row of each block.
-  static constexpr int kScales = GLU ? 1 + NB / 2 : 1;
-  __device__ __forceinline__ static constexpr int scale_of(int b) {
-    return GLU && b >= NB / 2 ? 1 + b - NB / 2 : 0;
-  }
-  static_assert(128 % WC == 0, "a wave's columns in one block of 128");
+  // scales of a step in LDS: for each wave row and column, 16 lanes' dwords
+  static constexpr int kA = (MB + 3) / 4, kB = (NB + 3) / 4;
+  static constexpr int kUnitsA = WM * 16 * kA, kUnits = kUnitsA + WN * 16 * kB;
+  // K steps whose scales LDS holds at a time
+  static constexpr int kScaleSteps = TM < 256 ? 32 : 64;
+  static constexpr int kLds = NS * kStage + kScaleSteps * kUnits * 4;
+  static_assert(kLds <= 160 * 1024, "LDS of a CU");
   static_assert(TM * RB % (1024 * kWaves) == 0 && TN * RB % (1024 * kWaves) == 0, "whole loads");
-  static_assert(!GLU || NB % 2 == 0, "gate and up blocks of a wave");
-  static_assert(NB % R == 0, "fragments keep their registers over the steps");
+  static_assert(MB % 2 == 0 && NB % 2 == 0, "halves");
 
   __device__ __forceinline__ static int swz(int r) { return (r >> 1) & 7; }
 
@@ -103,7 +123,7 @@ struct Gemm8 {
   int cha[kVarA], chb[kVarB];
   uint32_t fa, fb;         // fragment base addresses (A rows, B rows of the wave)
   uint32_t fs[2];          // lane's offset of the halves of a fragment
-  uint32_t sa, sb;         // the lane's rows in the scales
+  uint32_t sa, sb;         // the lane's dwords in a step's scales
 
   // Row of the expert's weights in LDS row r of the B operand, or -1.
   __device__ __forceinline__ static int64_t w_row(const TileAt& at, int r, int F) {
@@ -123,7 +143,7 @@ struct Gemm8 {
       : args(a8) {
     const ForwardArgs& a = a8.f;
     lds = (uint32_t)(uintptr_t)smem;
-    scales = lds + kStages;
+    scales = lds + NS * kStage;
     lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     wm = wave / WN;
@@ -131,9 +151,9 @@ struct Gemm8 {
     kbytes = a.d_in;
     nk = (kbytes + RB - 1) / RB;
     k0 = 0;
-    const int groups = nk / 4 < 16 ? nk / 4 : 16;
-    if constexpr (!FAR)
-      if (groups > 1) k0 = (at.e * 64 + at.col) * kStaggerGroups % groups * 4;
+    // (a longer loop goes by runs of kScaleSteps, from the first one on)
+    if constexpr (!FAR && TM < 256)
+      if (nk <= kScaleSteps) k0 = (at.e * 64 + at.col) * kStagger % nk;
     const int F = GLU ? a.d_out / 2 : a.d_out;
     const char* W = static_cast<const char*>(a.W) + (int64_t)at.e * a.d_out * kbytes;
     const char* x = static_cast<const char*>(a.x);
@@ -181,8 +201,8 @@ struct Gemm8 {
     for (int h = 0; h < 2; ++h) fs[h] = fr * RB + (((h * 4 + lane / MI) ^ swz(fr)) << 4);
     fa = lds + wm * WR * RB;
     fb = lds + TM * RB + wn * WC * RB;
-    sa = scales + (wm * WR + fr) * kScalePitch * 4;
-    sb = scales + (TM + wn * WC + fr) * kScalePitch * 4;
+    sa = scales + (wm * 16 + fr) * kA * 4;
+    sb = scales + (kUnitsA + (wn * 16 + fr) * kB) * 4;
   }
 
   __device__ __forceinline__ int chunk_of(int j) const {
@@ -207,36 +227,81 @@ struct Gemm8 {
     }
   }
 
-  // The scales of K steps first .. first + kScaleSteps - 1 of all the tile's rows
-  // into LDS; 1 for rows and steps that are not there (their values are zeros).
-  __device__ __forceinline__ void fill_scales(const TileAt& at, int first) const {
+  // Scales come into LDS four row blocks by four steps at a time.  A thread has four
+  // rows of its own, the same ones for all its steps; null: not there (its values are
+  // zeros, its scales 1).
+  static constexpr int kSide = kThreads / kUnits;   // groups of four steps at once
+  static_assert(kSide >= 1, "rows for every thread");
+  struct ScaleRows {
+    const uint8_t* p[4];
+  };
+  __device__ __forceinline__ ScaleRows scale_rows(const TileAt& at) const {
     const ForwardArgs& a = args.f;
-    constexpr int kDwords = kScaleSteps / 4;
     const int F = GLU ? a.d_out / 2 : a.d_out;
     const int pitch = fp8_scale_row(a.d_in);
-    const uint8_t* ws = args.ws + (int64_t)at.e * scale_blocks(a.d_out) * pitch;
-    for (int i = threadIdx.x; i < (TM + TN) * kDwords; i += kThreads) {
-      const int r = i / kDwords, j = i % kDwords;
-      const uint8_t* p = nullptr;
-      if (first + 4 * j < nk) {
-        if (r < TM) {
-          if (r < at.rows) {
-            const int64_t n = a.row_index != nullptr ? (int64_t)a.row_index[at.lo + r] : at.lo + r;
-            if (n >= 0 && n < a.T) p = args.xs + n * pitch;
-          }
-        } else {
-          const int64_t n = w_row(at, r - TM, F);
-          if (n >= 0) p = ws + n / kFp8Block * pitch;
+    const int unit = threadIdx.x % kUnits;
+    ScaleRows s;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      s.p[q] = nullptr;
+      if (unit < kUnitsA) {
+        const int b = unit % kA * 4 + q, r = unit / (16 * kA) * WR + b * MI + unit / kA % 16;
+        if (b < MB && r < at.rows) {
+          const int64_t n = a.row_index != nullptr ? (int64_t)a.row_index[at.lo + r] : at.lo + r;
+          if (n >= 0 && n < a.T) s.p[q] = args.xs + n * pitch;
         }
+      } else {
+        const int u = unit - kUnitsA;
+        const int b = u % kB * 4 + q, r = u / (16 * kB) * WC + b * MI + u / kB % 16;
+        const int64_t n = b < NB ? w_row(at, r, F) : -1;
+        if (n >= 0)
+          s.p[q] = args.ws + ((int64_t)at.e * scale_blocks(a.d_out) + n / kFp8Block) * pitch;
       }
-      const uint32_t w =
-          p != nullptr ? *reinterpret_cast<const uint32_t*>(p + first + 4 * j) : 0x7F7F7F7Fu;
-      *reinterpret_cast<LDS_AS uint32_t*>(
-          (LDS_AS char*)(uintptr_t)(scales + (r * kScalePitch + j) * 4)) = w;
+    }
+    return s;
+  }
+  // Those of K steps first .. first + kScaleSteps - 1, kBatch groups under way together.
+  __device__ __forceinline__ void fill_scales(const ScaleRows& s, int first) const {
+    constexpr int kGroups = kScaleSteps / 4, kBatch = 4;
+    const int unit = threadIdx.x % kUnits, j0 = threadIdx.x / kUnits;
+    if (j0 >= kSide) return;
+    const int groups = (nk - first + 3) / 4;
+    for (int j = j0; j < kGroups && j < groups; j += kSide * kBatch) {
+      uint32_t w[kBatch][4];
+#pragma unroll
+      for (int c = 0; c < kBatch; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          w[c][q] = 0x7F7F7F7Fu;
+          if (s.p[q] != nullptr && j + c * kSide < groups)
+            w[c][q] = *reinterpret_cast<const uint32_t*>(s.p[q] + first + 4 * (j + c * kSide));
+        }
+#pragma unroll
+      for (int c = 0; c < kBatch; ++c) {
+        flip_bytes(w[c]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (j + c * kSide < kGroups)
+            *reinterpret_cast<LDS_AS uint32_t*>((LDS_AS char*)(uintptr_t)(
+                scales + ((4 * (j + c * kSide) + q) * kUnits + unit) * 4)) = w[c][q];
+      }
     }
   }
   __device__ __forceinline__ static uint32_t read_dword(uint32_t addr) {
     return *reinterpret_cast<LDS_AS const uint32_t*>((LDS_AS char*)(uintptr_t)addr);
+  }
+
+  struct Scales {
+    uint32_t x[kA], w[kB];
+  };
+  __device__ __forceinline__ Scales read_scales(int k) const {
+    const uint32_t at = k % kScaleSteps * (kUnits * 4);
+    Scales s;
+#pragma unroll
+    for (int i = 0; i < kA; ++i) s.x[i] = read_dword(sa + at + 4 * i);
+#pragma unroll
+    for (int i = 0; i < kB; ++i) s.w[i] = read_dword(sb + at + 4 * i);
+    return s;
   }
 
   __device__ __forceinline__ Frag frag(uint32_t base, int buf, int i) const {
@@ -244,46 +309,59 @@ struct Gemm8 {
     return Frag{read_lds16(at + fs[0]), read_lds16(at + fs[1])};
   }
 
-  // One K step.  Its A fragments and its first R B fragments are in registers.  First
-  // the B blocks whose registers the step's other B blocks then take.  Then the
-  // barrier: all of this stage is in registers, the next stage's loads (the oldest
-  // ones) are in LDS; its fragments are read as registers come free, A row block
-  // by A row block, and the loads of step kt + NS go out over the stage.
-  static constexpr int kLate = MB * R;    // products behind the barrier
-  __device__ __forceinline__ static constexpr int spread(int i, int n, int span) {
-    return i >= span ? n : i * n / span;
+  // One K step, in four quarters of the products: a half of the A blocks by a half of
+  // the B blocks.  Even steps take (a0 b0) (a0 b1) (a1 b1) (a1 b0), odd ones (a0 b1)
+  // (a0 b0) (a1 b0) (a1 b1), so that each quarter lacks one half of the fragments, which has
+  // been read in the quarter before into registers that were free:
+  //   quarter 0   the other half of B, of this stage
+  //   quarter 1   a1, of this stage; then nobody reads it any more
+  //   quarter 2   a0, of the next stage
+  //   quarter 3   the half of B that the next step starts with
+  // LDS reads are as even over the step as that.  (All of a step's fragments in
+  // registers at its start, the next ones read in its last row of products: the reads
+  // of the four SIMDs then come at once, and 8192^3 took 911 thousand cycles.)
+  // Between quarters 1 and 2 the barrier: this stage is free for the loads of step kt +
+  // NS, which go out over the second half, and the next stage's loads are in LDS.
+  static constexpr int N = MB * NB, Q = N / 4;
+  static constexpr int MH = MB / 2, NH = NB / 2;
+  // Loads of a step that are out before product i.
+  __device__ __forceinline__ static constexpr int issued(int i) {
+    return i <= N / 2 ? 0 : (i - N / 2) * kLoads / (N / 2);
   }
-  __device__ __forceinline__ void round(int kt, int S, Frag (&a_)[MB], Frag (&b_)[R],
-                                        uint32_t (&xs_)[MB], uint32_t (&ws_)[kScales],
-                                        f32x4 (&acc)[MB][NB]) {
+  // The product of a quarter behind which fragment f of n is read: early enough to
+  // be back when the next quarter starts.
+  __device__ __forceinline__ static constexpr int read_at(int f, int n) { return f * Q * 3 / 4 / n; }
+
+  template <int ODD>
+  __device__ __forceinline__ void round(int kt, int next, int S, Frag (&a_)[MB], Frag (&b_)[NB],
+                                        Scales& sc, f32x4 (&acc)[MB][NB]) {
     const int SN = S + 1 == NS ? 0 : S + 1;
-    __builtin_amdgcn_s_setprio(1);
-    static_for<(NB - R) * MB>([&](auto i_) __attribute__((always_inline)) {
-      constexpr int i = i_, b = i / MB, a = i % MB;
-      acc[a][b] = mfma(b_[b % R], a_[a], acc[a][b], ws_[scale_of(b)], xs_[a]);
-      if constexpr (a == MB - 1) b_[b % R] = frag(fb, S, b + R);
-      __builtin_amdgcn_sched_barrier(0);
-    });
-    __builtin_amdgcn_s_setprio(0);
-    wait_loads_barrier<(NS - 2) * kLoads>();
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_setprio(1);
-    static_for<kLate>([&](auto i_) __attribute__((always_inline)) {
-      constexpr int i = i_, a = i / R, q = i % R, b = NB - R + q;
-      acc[a][b] = mfma(b_[q], a_[a], acc[a][b], ws_[scale_of(b)], xs_[a]);
-      if constexpr (q == R - 1) a_[a] = frag(fa, SN, a);
-      if constexpr (a == MB - 1) b_[q] = frag(fb, SN, q);
-      constexpr int l0 = spread(i, kLoads, kLate), l1 = spread(i + 1, kLoads, kLate);
-      static_for<l1 - l0>([&](auto l) __attribute__((always_inline)) {
-        issue(l0 + l, S, kt + NS);
+    Scales ahead;
+    static_for<N>([&](auto i_) __attribute__((always_inline)) {
+      constexpr int i = i_, q = i / Q, r = i % Q;
+      constexpr int bh = (q == 1 || q == 2) != (ODD != 0);
+      constexpr int a = (q >= 2 ? MH : 0) + r / NH, b = bh * NH + r % NH;
+      if constexpr (i == N / 2) {
+        wait_loads_barrier<(NS - 2) * kLoads>();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      acc[a][b] = mfma<b % 4, a % 4>(b_[b], a_[a], acc[a][b], sc.w[b / 4], sc.x[a / 4]);
+      static_for<(q == 1 || q == 2) ? MH : NH>([&](auto f_) __attribute__((always_inline)) {
+        constexpr int f = f_;
+        if constexpr (r == read_at(f, (q == 1 || q == 2) ? MH : NH)) {
+          if constexpr (q == 0) b_[(1 - ODD) * NH + f] = frag(fb, S, (1 - ODD) * NH + f);
+          if constexpr (q == 1) a_[MH + f] = frag(fa, S, MH + f);
+          if constexpr (q == 2) a_[f] = frag(fa, SN, f);
+          if constexpr (q == 3) b_[(1 - ODD) * NH + f] = frag(fb, SN, (1 - ODD) * NH + f);
+        }
+      });
+      if constexpr (i == N / 2) ahead = read_scales(next);
+      static_for<issued(i + 1) - issued(i)>([&](auto l) __attribute__((always_inline)) {
+        issue(issued(i) + l, S, kt + NS);
       });
       __builtin_amdgcn_sched_barrier(0);
     });
-    __builtin_amdgcn_s_setprio(0);
-#pragma unroll
-    for (int a = 0; a < MB; ++a) xs_[a] >>= 8;
-#pragma unroll
-    for (int b = 0; b < kScales; ++b) ws_[b] >>= 8;
+    sc = ahead;
   }
 
   __device__ __forceinline__ void mainloop(const TileAt& at, f32x4 (&acc)[MB][NB]) {
@@ -291,39 +369,132 @@ struct Gemm8 {
     for (int a = 0; a < MB; ++a)
 #pragma unroll
       for (int b = 0; b < NB; ++b) acc[a][b] = f32x4{};
+    // the scales' loads beside the first stage's, which the products wait for as well
+    const ScaleRows rows = scale_rows(at);
 #pragma unroll
-    for (int d = 0; d < NS; ++d)
+    for (int j = 0; j < kLoads; ++j) issue(j, 0, 0);
+    fill_scales(rows, 0);
+#pragma unroll
+    for (int d = 1; d < NS; ++d)
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) issue(j, d, d);
-    fill_scales(at, k0 / kScaleSteps * kScaleSteps);
     wait_loads_barrier<(NS - 1) * kLoads>();
-    Frag a_[MB], b_[R];
+    Frag a_[MB], b_[NB];
 #pragma unroll
-    for (int i = 0; i < MB; ++i) a_[i] = frag(fa, 0, i);
+    for (int i = 0; i < MH; ++i) a_[i] = frag(fa, 0, i);
 #pragma unroll
-    for (int i = 0; i < R; ++i) b_[i] = frag(fb, 0, i);
-    uint32_t xs_[MB], ws_[kScales];
+    for (int i = 0; i < NH; ++i) b_[i] = frag(fb, 0, i);
+    Scales sc = read_scales(k0);
     int S = 0, k = k0;   // k: the K step of this turn
-    for (int kt = 0; kt < nk; ++kt) {
-      if (k % 4 == 0) {
-        if (k % kScaleSteps == 0 && nk > kScaleSteps && kt > 0) {
-          // everybody has read the last of the old ones before the barrier of the
-          // step that has just ended
-          fill_scales(at, k);
-          __syncthreads();
-        }
-        const uint32_t j = k % kScaleSteps / 4 * 4;
-#pragma unroll
-        for (int i = 0; i < MB; ++i) xs_[i] = read_dword(sa + i * MI * kScalePitch * 4 + j);
-#pragma unroll
-        for (int i = 0; i < kScales; ++i)
-          ws_[i] = read_dword(sb + (i == 0 ? 0 : NB / 2 + i - 1) * MI * kScalePitch * 4 + j);
+    for (int kt = 0;;) {
+      const int end = nk - kt < kScaleSteps ? nk : kt + kScaleSteps;
+      for (; kt + 1 < end; kt += 2) {
+        k = k + 1 == nk ? 0 : k + 1;
+        round<0>(kt, k, NS == 2 ? 0 : S, a_, b_, sc, acc);
+        S = S + 1 == NS ? 0 : S + 1;
+        k = k + 1 == nk ? 0 : k + 1;
+        round<1>(kt + 1, k, NS == 2 ? 1 : S, a_, b_, sc, acc);
+        S = S + 1 == NS ? 0 : S + 1;
       }
-      round(kt, S, a_, b_, xs_, ws_, acc);
-      S = S + 1 == NS ? 0 : S + 1;
-      k = k + 1 == nk ? 0 : k + 1;
+      if (kt < end) {   // the last one of an odd number
+        round<0>(kt, 0, NS == 2 ? 0 : S, a_, b_, sc, acc);
+        ++kt;
+      }
+      if (kt >= nk) break;
+      // everybody has read the last of the old ones before the last step's barrier
+      fill_scales(scale_rows(at), kt);
+      __syncthreads();
+      sc = read_scales(kt);
     }
-    wait_loads_barrier<0>();   // the stages become the epilogue's staging
+    // nobody reads LDS any more, and nothing is on its way there
+    wait_loads_barrier<0>();
+  }
+
+  // Epilogue from registers: 16 rows and 32 columns at a time, 64 bytes of a row; bias,
+  // activation and residual in float32, one rounding.  It is straight-line code, which the
+  // instruction cache has to take in for each tile: one activation's at a time.
+  static constexpr int kOutBlocks = GLU ? NB / 2 : NB;
+  static constexpr int CW = kOutBlocks % 2 == 0 ? 8 : 4;   // columns of a lane
+  static constexpr int kPieces = kOutBlocks * 4 / CW;      // lanes' pieces of a row
+  typedef std::conditional_t<CW == 8, vec4u, uint2> Piece;
+  // Columns CW * g .. of piece p in lane group g, from block `first` of the results on.
+  __device__ __forceinline__ static void columns(const f32x4 (&row)[NB], int first, int p,
+                                                 float (&v)[CW]) {
+    if constexpr (CW == 8) {
+      eight_columns(row[first + 2 * p], row[first + 2 * p + 1], v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = row[first + p][i];
+    }
+  }
+  __device__ __forceinline__ static void add(float (&v)[CW], const Piece& w) {
+    const uint32_t* d = reinterpret_cast<const uint32_t*>(&w);
+#pragma unroll
+    for (int j = 0; j < CW / 2; ++j) {
+      v[2 * j] += __uint_as_float(d[j] << 16);
+      v[2 * j + 1] += __uint_as_float(d[j] & 0xFFFF0000u);
+    }
+  }
+  __device__ __forceinline__ static Piece piece(const void* p, int64_t o) {
+    return *reinterpret_cast<const Piece*>(static_cast<const uint16_t*>(p) + o);
+  }
+  __device__ __forceinline__ static void put(void* p, int64_t o, const float (&v)[CW]) {
+    Piece w;
+    uint32_t* d = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+    for (int j = 0; j < CW / 2; ++j) d[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+    *reinterpret_cast<Piece*>(static_cast<uint16_t*>(p) + o) = w;
+  }
+
+  __device__ __forceinline__ void epilogue(const TileAt& at, const f32x4 (&acc)[MB][NB]) const {
+    if constexpr (GLU) return finish<LRMOE_ACT_SWIGLU>(at, acc);
+    switch (args.f.act) {
+      case LRMOE_ACT_RELU: return finish<LRMOE_ACT_RELU>(at, acc);
+      case LRMOE_ACT_SILU: return finish<LRMOE_ACT_SILU>(at, acc);
+      case LRMOE_ACT_GELU: return finish<LRMOE_ACT_GELU>(at, acc);
+      default: return finish<LRMOE_ACT_NONE>(at, acc);
+    }
+  }
+  template <int ACT>
+  __device__ __forceinline__ void finish(const TileAt& at, const f32x4 (&acc)[MB][NB]) const {
+    const ForwardArgs& a = args.f;
+    const int F = GLU ? a.d_out / 2 : a.d_out;
+    const int col = at.col * kOut + wn * kOutBlocks * MI + lane / MI * CW;
+    const int64_t bias = (int64_t)at.e * a.d_out + col;
+    static_for<MB>([&](auto i_) __attribute__((always_inline)) {
+      constexpr int i = i_;
+      const int r0 = wm * WR + i * MI;
+      if (r0 >= at.rows) return;   // wave-uniform
+      const bool row_ok = r0 + lane % MI < at.rows;
+      const int64_t o = (at.lo + r0 + lane % MI) * F + col;
+      Piece res[kPieces];
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p)
+        if (a.residual != nullptr && row_ok && col + 4 * CW * p < F)
+          res[p] = piece(a.residual, o + 4 * CW * p);
+      static_for<kPieces>([&](auto p_) __attribute__((always_inline)) {
+        constexpr int p = p_, c = 4 * CW * p;
+        const bool ok = row_ok && col + c < F;
+        float z[CW], v[CW];
+        columns(acc[i], 0, p, z);
+        if (a.bias != nullptr && ok) add(z, piece(a.bias, bias + c));
+        if (a.pre_a != nullptr && ok) put(a.pre_a, o + c, z);
+        if constexpr (GLU) {
+          float w[CW];
+          columns(acc[i], NB / 2, p, w);
+          if (a.bias != nullptr && ok) add(w, piece(a.bias, bias + F + c));
+          if (a.pre_b != nullptr && ok) put(a.pre_b, o + c, w);
+#pragma unroll
+          for (int j = 0; j < CW; ++j) v[j] = z[j] * sigmoid_f32(z[j]) * w[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < CW; ++j) v[j] = z[j];
+          activate(ACT, v);
+        }
+        if (a.residual != nullptr && ok) add(v, res[p]);
+        if (ok) put(a.y, o + c, v);
+      });
+    });
   }
 };
 
@@ -333,7 +504,7 @@ __device__ __forceinline__ void run_tile(const Fp8Args& args, const TileAt& at,
   G g(args, at, smem);
   f32x4 acc[G::kMB][G::kNB];
   g.mainloop(at, acc);
-  G::Epi::run(args.f, at, acc, g.lds, g.lane, g.wave);
+  g.epilogue(at, acc);
 }
 
 template <typename G>
@@ -347,19 +518,20 @@ __global__ __launch_bounds__(G::kThreads, G::kWavesPerSimd) void gemm8_kernel(Fp
 
 template <bool GLU>
 struct Ragged8 {
-  typedef Gemm8<64, 128, 4, 2, 2, GLU> G256;
-  typedef Gemm8<64, 64, 2, 4, 3, GLU> G128;
-  typedef Gemm8<32, 64, 2, 4, 3, GLU> G64;
+  typedef Gemm8<128, 128, 2, 2, 2, GLU> G256;
+  typedef Gemm8<64, 128, 2, 2, 3, GLU> G128;
+  typedef Gemm8<32, 128, 2, 2, 3, GLU> G64;
   static constexpr int kLds = std::max(std::max(G256::kLds, G128::kLds), G64::kLds);
   static constexpr int kThreads = G256::kThreads, kOut = G256::kOut;
 };
 
 template <bool GLU>
-__global__ __launch_bounds__(512, 2) void ragged_gemm8_kernel(Fp8Args args, int cols) {
+__global__ __launch_bounds__(256, 1) void ragged_gemm8_kernel(Fp8Args args, int cols) {
   typedef Ragged8<GLU> R;
   __shared__ __attribute__((aligned(16))) char smem[R::kLds];
   TileAt at;
-  if (!find_ragged_tile(args.f.seg, args.f.E, args.f.P, cols, at)) return;
+  if (!find_ragged_tile(args.f.seg, args.f.E, args.f.P, cols, blockIdx.x, at) || at.rows <= 0)
+    return;
   if (at.rows > 128) run_tile<typename R::G256>(args, at, (LDS_AS char*)smem);
   else if (at.rows > 64) run_tile<typename R::G128>(args, at, (LDS_AS char*)smem);
   else run_tile<typename R::G64>(args, at, (LDS_AS char*)smem);
@@ -435,11 +607,11 @@ __global__ __launch_bounds__(256) void few_rows8_kernel(Fp8Args a8, int cols) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) sw[c] = dword(ws[c], g);
     sx = dword(xs, g);
+    static_for<4>([&](auto u_) __attribute__((always_inline)) {
+      constexpr int u = u_;
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-        acc[c] = mfma(w[u][c], x[u], acc[c], sw[c] >> (8 * u), sx >> (8 * u));
+      for (int c = 0; c < NC; ++c) acc[c] = mfma<u, u>(w[u][c], x[u], acc[c], sw[c], sx);
+    });
   }
 #pragma unroll
   for (int c = 0; c < NC; ++c)

@@ -14,6 +14,7 @@ namespace {
 #define LDS_AS __attribute__((address_space(3)))
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 __device__ const vec4u zero_page[16] = {};
 
@@ -106,8 +107,10 @@ __device__ __forceinline__ bool find_tile(const int32_t* seg, int E, int64_t P, 
 
 constexpr int kXcds = 8, kXcdCus = 32;
 
+// Tile of workgroup `block` of the launch, false behind the last one.  A piece of a cut
+// tile may have no rows.
 __device__ __forceinline__ bool find_ragged_tile(const int32_t* seg, int E, int64_t P, int cols,
-                                                 TileAt& at) {
+                                                 int64_t block, TileAt& at) {
   const int lane = threadIdx.x & 63;
   int64_t off[5];
 #pragma unroll
@@ -135,8 +138,8 @@ __device__ __forceinline__ bool find_ragged_tile(const int32_t* seg, int E, int6
   const int fend = wave_scan(full), pend = wave_scan(part);
   const int fulls = __builtin_amdgcn_readlane(fend, 63);
   const int parts = __builtin_amdgcn_readlane(pend, 63);
-  const int x = blockIdx.x % kXcds;
-  const int64_t pos = blockIdx.x / kXcds;
+  const int x = block % kXcds;
+  const int64_t pos = block / kXcds;
   const int64_t ft = (int64_t)fulls * cols, pt = (int64_t)parts * cols;
   const int64_t f0 = ft * x / kXcds, f1 = ft * (x + 1) / kXcds;   // this XCD's share
   const int64_t p0 = pt * x / kXcds, p1 = pt * (x + 1) / kXcds;
@@ -168,7 +171,8 @@ __device__ __forceinline__ bool find_ragged_tile(const int32_t* seg, int E, int6
   r = __builtin_amdgcn_readfirstlane(r);
   at.col = __builtin_amdgcn_readfirstlane(at.col);
   const unsigned long long past = whole ? __ballot(fend > r) : __ballot(pend > r);
-  if (past == 0) return false;
+  at.rows = 0;
+  if (past == 0) return true;   // offsets out of order
   const int owner = __ffsll(past) - 1;
   int sub = whole ? r - (fend - full) : r - (pend - part), j = 0;   // meant for the owner lane
   const bool sane = sub >= 0;
@@ -189,7 +193,7 @@ __device__ __forceinline__ bool find_ragged_tile(const int32_t* seg, int E, int6
   at.e = __builtin_amdgcn_readlane(4 * lane + j, owner);
   at.lo = (uint32_t)__builtin_amdgcn_readlane((uint32_t)(oj + first), owner);   // P < 2^31
   at.rows = __builtin_amdgcn_readlane(rows, owner);
-  return at.rows > 0;
+  return true;
 }
 
 // ---- global -> LDS, 16 bytes a lane: lane i writes LDS bytes [lds + 16 i,
@@ -238,13 +242,13 @@ __device__ __forceinline__ vec4u read_lds16(uint32_t addr) {
   return *reinterpret_cast<LDS_AS const vec4u*>((LDS_AS char*)(uintptr_t)addr);
 }
 
-// Epilogue of a tile whose waves (WM x WN) hold WR x WC results each, in 16 x 16
+// Epilogue of a tile whose waves (WM x WN) hold WR x WC results each, in MI x MI
 // blocks: 32 rows at a time through the wave's own LDS region, so that rows leave
 // in whole 16-byte pieces; bias, activation and residual in float32, one rounding
 // to O.
-template <typename O, int WR, int WC, int WM, int WN, bool GLU>
+template <typename O, int WR, int WC, int WM, int WN, bool GLU, int MI = 16>
 struct Epilogue {
-  static constexpr int MI = 16;
+  typedef std::conditional_t<MI == 16, f32x4, f32x16> Acc;
   static constexpr int MB = WR / MI, NB = WC / MI;
   static constexpr int kOut = GLU ? WN * WC / 2 : WN * WC;
   static constexpr int kLds = WM * WN * WC * 128;
@@ -264,7 +268,7 @@ struct Epilogue {
 
   // lds: address of the staging of all waves
   __device__ __forceinline__ static void run(const ForwardArgs& args, const TileAt& at,
-                                             const f32x4 (&acc)[MB][NB], uint32_t lds, int lane,
+                                             const Acc (&acc)[MB][NB], uint32_t lds, int lane,
                                              int wave) {
     const int wm = wave / WN, wn = wave % WN;
     const int F = GLU ? args.d_out / 2 : args.d_out;
@@ -288,12 +292,20 @@ struct Epilogue {
       constexpr int a = a_ * G;
       const int r0 = wm * WR + a * MI;
       if (r0 < at.rows) {   // wave-uniform
+        // a lane holds 4 columns of one row, of 32 x 32 blocks four times
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
-          for (int b = 0; b < NB; ++b)   // a lane holds 4 columns of one row
-            *reinterpret_cast<LDS_AS f32x4*>((LDS_AS char*)(uintptr_t)(
-                base + epi_off(g * MI + lane % MI, b * (MI / 4) + lane / 16))) = acc[a + g][b];
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int q = 0; q < MI * MI / 256; ++q) {
+              f32x4 v;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[i] = acc[a + g][b][4 * q + i];
+              *reinterpret_cast<LDS_AS f32x4*>((LDS_AS char*)(uintptr_t)(
+                  base + epi_off(g * MI + lane % MI,
+                                 b * (MI / 4) + q * (64 / MI) + lane / MI))) = v;
+            }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         for (int p = 0; p < 32 / per; ++p) {
