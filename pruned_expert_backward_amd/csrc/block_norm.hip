@@ -55,24 +55,44 @@ struct RowSum {
   }
 };
 
+template <typename T>
+__device__ __forceinline__ void unpack(const vec4u& w, float (&v)[kPiece<T>]) {
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(w[j]);
+  }
+}
+
 // Piece i of this lane starts at column at(i).
 template <typename T, int WPR, int PIECES>
 struct Row {
   static constexpr int N = kPiece<T>;
-  static constexpr int kWaves = WPR > 4 ? WPR : 4;      // waves of a workgroup
+  static constexpr int kWaves = WPR > 1 ? WPR : 4;      // waves of a workgroup: one row, or
+                                                        // four rows without barriers
   static constexpr int kRows = kWaves / WPR;            // rows it works on at once
   static constexpr int kWidth = WPR * 64 * PIECES * N;  // columns it can hold
   __device__ __forceinline__ static int at(int i) {
     return (i * WPR * 64 + (int)(threadIdx.x % (WPR * 64))) * N;
   }
+  // A row as it is stored (null: zeros), and its values.
   __device__ __forceinline__ static void load(const void* p, int64_t row, int D,
-                                              float (&v)[PIECES][N]) {
+                                              vec4u (&w)[PIECES]) {
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-#pragma unroll
-      for (int j = 0; j < N; ++j) v[i][j] = 0.f;
-      if (at(i) < D) load_vals(static_cast<const T*>(p) + row * D + at(i), v[i]);
+      w[i] = vec4u{};
+      if (p != nullptr && at(i) < D)
+        w[i] = *reinterpret_cast<const vec4u*>(static_cast<const T*>(p) + row * D + at(i));
     }
+  }
+  __device__ __forceinline__ static void values(const vec4u (&w)[PIECES], float (&v)[PIECES][N]) {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) unpack<T>(w[i], v[i]);
   }
   __device__ __forceinline__ static void store(void* p, int64_t row, int D,
                                                const float (&v)[PIECES][N]) {
@@ -86,18 +106,7 @@ struct Row {
 template <typename T, int PIECES>
 struct Weight {
   vec4u w[PIECES];
-  __device__ __forceinline__ void get(int i, float (&v)[kPiece<T>]) const {
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = __uint_as_float(w[i][j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[i][j] & 0xFFFF0000u);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(w[i][j]);
-    }
-  }
+  __device__ __forceinline__ void get(int i, float (&v)[kPiece<T>]) const { unpack<T>(w[i], v); }
   template <typename R>
   __device__ __forceinline__ void load(const void* p, int D) {
     constexpr uint32_t one = sizeof(T) == 2 ? 0x3F803F80u : 0x3F800000u;
@@ -115,7 +124,7 @@ __device__ __forceinline__ float inv_rms(float sumsq, int D, float eps) {
 }
 
 template <typename T, int WPR, int PIECES>
-__global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(NormArgs a, void* s,
+__global__ __launch_bounds__(64 * (WPR > 1 ? WPR : 4)) void norm_kernel(NormArgs a, void* s,
                                                                         void* h) {
   typedef Row<T, WPR, PIECES> R;
   constexpr int N = R::N;
@@ -125,14 +134,18 @@ __global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(NormArgs
   wb.template load<R>(a.branch_weight, a.D);
   gc.template load<R>(a.gate_kind == LRMOE_BRANCH_GATE_CHANNEL ? a.gate : nullptr, a.D);
   w.template load<R>(a.weight, a.D);
-  const int mine = WPR > 1 ? 0 : threadIdx.x >> 6;
+  const int mine = threadIdx.x / (WPR * 64);
   for (int64_t row = (int64_t)blockIdx.x * R::kRows + mine; row < a.T;
        row += (int64_t)gridDim.x * R::kRows) {
-    float x[PIECES][N];
-    R::load(a.x, row, a.D, x);
+    float x[PIECES][N], y[PIECES][N];
+    {
+      vec4u wx[PIECES], wy[PIECES];
+      R::load(a.x, row, a.D, wx);
+      R::load(a.y, row, a.D, wy);
+      R::values(wx, x);
+      R::values(wy, y);
+    }
     if (a.y != nullptr) {
-      float y[PIECES][N];
-      R::load(a.y, row, a.D, y);
       float r = a.gate_kind == LRMOE_BRANCH_GATE_TOKEN ? static_cast<const float*>(a.gate)[row]
                                                        : 1.f;
       if (a.branch_weight != nullptr) {
@@ -175,13 +188,12 @@ __global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_kernel(NormArgs
 }
 
 // ---- gradient
-// Groups of waves that a gradient call has (the workspace has a row of sums for
-// each), and its sums over rows, in this order: dw, dw_b, dg.
-constexpr int kGroups = 1024;
+// Groups of waves (one for a row) have a row of sums each in the workspace; its three
+// kinds: dw, dw_b, dg.
 constexpr int kSums = 3;
 
 template <typename T, int WPR, int PIECES>
-__global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_grad_kernel(
+__global__ __launch_bounds__(64 * (WPR > 1 ? WPR : 4)) void norm_grad_kernel(
     NormArgs a, const void* ds, const void* dh, void* dx, void* dy, float* dgate, float* ws,
     int sums) {
   typedef Row<T, WPR, PIECES> R;
@@ -202,21 +214,24 @@ __global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_grad_kernel(
     for (int i = 0; i < PIECES; ++i)
 #pragma unroll
       for (int j = 0; j < N; ++j) acc[k][i][j] = 0.f;
-  const int mine = WPR > 1 ? 0 : threadIdx.x >> 6;
+  const int mine = threadIdx.x / (WPR * 64);
   const int64_t group = (int64_t)blockIdx.x * R::kRows + mine;
-  for (int64_t row = group; row < a.T; row += (int64_t)gridDim.x * R::kRows) {
+  const int64_t stride = (int64_t)gridDim.x * R::kRows;
+  vec4u wd[PIECES], we[PIECES], wx[PIECES], wy[PIECES];
+  auto fetch = [&](int64_t row) __attribute__((always_inline)) {
+    R::load(ds, row, a.D, wd);
+    R::load(dh, row, a.D, we);
+    R::load(norm ? a.x : nullptr, row, a.D, wx);
+    R::load(a.y, row, a.D, wy);
+  };
+  if (group < a.T) fetch(group);
+  for (int64_t row = group; row < a.T; row += stride) {
     float d[PIECES][N], x[PIECES][N], y[PIECES][N], e[PIECES][N];
-    if (ds != nullptr) R::load(ds, row, a.D, d);
-    else
-#pragma unroll
-      for (int i = 0; i < PIECES; ++i)
-#pragma unroll
-        for (int j = 0; j < N; ++j) d[i][j] = 0.f;
-    if (norm) {
-      R::load(dh, row, a.D, e);
-      R::load(a.x, row, a.D, x);
-    }
-    if (a.y != nullptr) R::load(a.y, row, a.D, y);
+    R::values(wd, d);
+    R::values(we, e);
+    R::values(wx, x);
+    R::values(wy, y);
+    if (row + stride < a.T) fetch(row + stride);   // under way while this row is worked on
     float q[3] = {0.f, 0.f, 0.f};   // s^2, dh w s, y^2
     if (norm) {
 #pragma unroll
@@ -300,33 +315,41 @@ __global__ __launch_bounds__(64 * (WPR > 4 ? WPR : 4)) void norm_grad_kernel(
   }
 }
 
-// Sums of all groups: a workgroup takes 64 columns of one sum, its 16 waves the
-// groups in turn.
+// Sums of all groups: a workgroup takes 32 columns of one kind, its 32 half waves the
+// groups in turn.  (512 rows of 2048: 15.5 us with the gradient, 20.6 with 16 columns, 16.1
+// with 64.)
 __global__ __launch_bounds__(1024) void norm_sums_kernel(const float* ws, int groups, int D,
                                                          float* dw, float* dwb, float* dg) {
-  __shared__ float part[16][64];
+  __shared__ float part[32][33];
   const int k = blockIdx.y;
   float* out = k == 0 ? dw : k == 1 ? dwb : dg;
   if (out == nullptr) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int col = blockIdx.x * 64 + lane;
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;
   float t = 0.f;
   if (col < D) {
 #pragma unroll 8
-    for (int g = wave; g < groups; g += 16) t += ws[((int64_t)g * kSums + k) * D + col];
+    for (int g = row; g < groups; g += 32) t += ws[((int64_t)g * kSums + k) * D + col];
   }
-  part[wave][lane] = t;
+  part[row][lane] = t;
   __syncthreads();
-  if (wave != 0 || col >= D) return;
+  if (threadIdx.x >= 32 || col >= D) return;
 #pragma unroll
-  for (int w = 1; w < 16; ++w) t += part[w][lane];
+  for (int r = 1; r < 32; ++r) t += part[r][lane];
   out[col] = t;
 }
+
+// Most groups of a gradient call, for rows of `wpr` waves: those that 256 CUs hold at
+// once, so that all rows are shared evenly.  12 waves a CU by their registers; of 8-wave
+// workgroups one, of 16-wave ones (held to 128 registers) one.  (16 waves a CU
+// throughout: 32768 x 2048 191 us, 163 like this; 32768 x 4096 310 and 294 us.)
+int grad_groups(int wpr) { return 256 * (wpr <= 4 ? 12 : wpr == 8 ? 8 : 16) / wpr; }
 
 // Workgroups of a gradient call (each of them R::kRows groups).
 template <typename R>
 int grad_blocks(int64_t T) {
-  return (int)std::min<int64_t>((T + R::kRows - 1) / R::kRows, kGroups / R::kRows);
+  return (int)std::min<int64_t>((T + R::kRows - 1) / R::kRows,
+                                grad_groups(R::kWaves / R::kRows) / R::kRows);
 }
 
 template <typename T, int WPR, int PIECES>
@@ -353,19 +376,27 @@ hipError_t norm_grad(const NormArgs& a, const void* ds, const void* dh, void* dx
     if (e != hipSuccess) return e;
   }
   if (sums == 0) return hipSuccess;
-  hipLaunchKernelGGL(norm_sums_kernel, dim3((a.D + 63) / 64, kSums), dim3(1024), 0, st, ws,
+  hipLaunchKernelGGL(norm_sums_kernel, dim3((a.D + 31) / 32, kSums), dim3(1024), 0, st, ws,
                      blocks * R::kRows, a.D, dweight, dbranch_weight, dg);
   return hipGetLastError();
 }
 
-// The narrowest shape that holds the row (columns in bf16; float32 half of them).
+// Waves of a row and pieces of a lane: the narrowest shape that holds the row (512
+// columns a wave in bf16 and, with twice the pieces, in float32; 16 waves and more pieces
+// for the widest).
 template <typename T, typename F>
 hipError_t by_width(int D, F&& f) {
-  constexpr int N = kPiece<T>, P = 8 / N;   // float32 takes twice the pieces
-  if (D <= 512) return f(std::integral_constant<int, 1>(), std::integral_constant<int, P>());
-  if (D <= 2048) return f(std::integral_constant<int, 4>(), std::integral_constant<int, P>());
-  if (D <= 8192) return f(std::integral_constant<int, 16>(), std::integral_constant<int, P>());
+  constexpr int P = 8 / kPiece<T>;
+  std::integral_constant<int, P> p;
+  if (D <= 512) return f(std::integral_constant<int, 1>(), p);
+  if (D <= 1024) return f(std::integral_constant<int, 2>(), p);
+  if (D <= 2048) return f(std::integral_constant<int, 4>(), p);
+  if (D <= 4096) return f(std::integral_constant<int, 8>(), p);
+  if (D <= 8192) return f(std::integral_constant<int, 16>(), p);
   return f(std::integral_constant<int, 16>(), std::integral_constant<int, 2 * P>());
+}
+int waves_of_row(int D) {
+  return D <= 512 ? 1 : D <= 1024 ? 2 : D <= 2048 ? 4 : D <= 4096 ? 8 : 16;
 }
 
 }  // namespace
@@ -380,7 +411,8 @@ hipError_t launch_residual_norm(int dtype, const NormArgs& a, void* s, void* h, 
 }
 
 size_t residual_norm_workspace(int64_t T, int32_t D) {
-  return (size_t)std::min<int64_t>((T + 3) / 4 * 4, kGroups) * kSums * D * sizeof(float);
+  return (size_t)std::min<int64_t>((T + 3) / 4 * 4, grad_groups(waves_of_row(D))) * kSums * D *
+         sizeof(float);
 }
 
 hipError_t launch_residual_norm_backward(int dtype, const NormArgs& a, const void* ds,

@@ -658,7 +658,7 @@ hipError_t forward(const Fp8Args& a, int F, bool far, hipStream_t s) {
   constexpr int h = GLU ? 2 : 1;   // W rows of an output column
   if (expected(a.f, F, 16, 32 / h) <= 320) return launch_few_rows<2, GLU>(a, F, s);
   if (far) return launch_gemm<Gemm8<32, 64, 2, 2, 3, GLU, true>>(a, F, s);
-  if (a.f.P <= (int64_t)16 * a.f.E && expected(a.f, F, 32, 256 / h) >= 160)
+  if (a.f.P <= (int64_t)32 * a.f.E && expected(a.f, F, 32, 256 / h) >= 160)
     return launch_gemm<Gemm8<32, 64, 1, 4, 3, GLU>>(a, F, s);
   if (expected(a.f, F, 32, 64 / h) <= 320)
     return launch_gemm<Gemm8<32, 32, 1, 2, 4, GLU>>(a, F, s);

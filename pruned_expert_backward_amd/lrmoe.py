@@ -7,6 +7,7 @@ call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes as C
 import functools
 import os
@@ -1233,26 +1234,40 @@ def adamw_step(params: Sequence, grads: Sequence, states: Sequence, step, lr,
     if count == 0:
         return
     dev = _device(params[0])
-    f32, u8 = torch.float32, torch.uint8
-    table = (AdamWTensor * count)()
-    for k in range(count):
-        p, g, st, a = params[k], grads[k], states[k], table[k]
-        n, shape = p.numel(), p.shape
-        a.n = n
-        a.p_dtype, a.g_dtype = storage_dtype(p.dtype), storage_dtype(g.dtype)
-        a.p = _arg("params", p, p.dtype, shape, dev)
-        a.g = _arg("grads", g, g.dtype, shape, dev)
+    f32, u8, bf16 = torch.float32, torch.uint8, torch.bfloat16
+    at = dev.index
+
+    def flat(name, x, dtype, n):
+        """_arg for n elements in one dimension, at less host time."""
+        if x.dtype is dtype and x.numel() == n and x.get_device() == at and x.dim() == 1 \
+                and x.is_contiguous():
+            return x.data_ptr()
+        return _arg(name, x, dtype, (n,), dev) or 0
+
+    def like(name, x, dtype, shape):
+        """_arg for a parameter's shape."""
+        if x.dtype is dtype and x.get_device() == at and x.is_contiguous() and x.shape == shape:
+            return x.data_ptr()
+        return _arg(name, x, dtype, shape, dev) or 0
+
+    # the descriptors as whole numbers, each one's two types in the last
+    rows = []
+    for k, (p, g, st) in enumerate(zip(params, grads, states)):
+        n, shape, pd, gd = p.numel(), p.shape, p.dtype, g.dtype
+        pt = 1 if pd is bf16 else 0 if pd is f32 else storage_dtype(pd)
+        gt = 1 if gd is bf16 else 0 if gd is f32 else storage_dtype(gd)
+        copy = None if copies is None else copies[k]
         if "root" in st:
-            b = (-(-n // FP8_BLOCK),)
-            a.m = _arg("m", st["m"], FP8, (n,), dev)
-            a.v = _arg("root", st["root"], FP8, (n,), dev)
-            a.m_scale = _arg("m_scale", st["m_scale"], u8, b, dev)
-            a.v_scale = _arg("root_scale", st["root_scale"], u8, b, dev)
+            b = -(-n // FP8_BLOCK)
+            moments = (flat("m", st["m"], FP8, n), flat("root", st["root"], FP8, n),
+                       flat("m_scale", st["m_scale"], u8, b),
+                       flat("root_scale", st["root_scale"], u8, b))
         else:
-            a.m = _arg("m", st["m"], f32, (n,), dev)
-            a.v = _arg("v", st["v"], f32, (n,), dev)
-        if copies is not None and copies[k] is not None:
-            a.copy = _arg("copies", copies[k], torch.bfloat16, shape, dev)
+            moments = flat("m", st["m"], f32, n), flat("v", st["v"], f32, n), 0, 0
+        rows += (n, like("params", p, pd, shape), like("grads", g, gd, shape), *moments,
+                 0 if copy is None else like("copies", copy, bf16, shape), pt | gt << 32)
+    host = array.array("q", rows)
+    table = (AdamWTensor * count).from_buffer(host)
     on_dev = isinstance(step, torch.Tensor), isinstance(lr, torch.Tensor)
     cfg = AdamW(0.0 if on_dev[1] else float(lr), float(betas[0]), float(betas[1]), float(eps),
                 float(weight_decay), 0 if on_dev[0] else int(step), int(seed) & 0xFFFFFFFF,
