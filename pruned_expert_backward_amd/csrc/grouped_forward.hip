@@ -68,6 +68,102 @@ __device__ __forceinline__ f32x4 mfma(vec4u a, vec4u b, f32x4 c) {
 // 87 us against 68 us for 369 MB of W; other strides are unchanged).
 constexpr int kStagger = 3;
 
+// Epilogue of a tile whose waves (WM x WN) hold WR x WC results each, in 16 x 16
+// blocks: 32 rows at a time through the wave's own LDS region, so that rows leave
+// in whole 16-byte pieces; bias, activation and residual in float32, one rounding
+// to O.
+template <typename O, int WR, int WC, int WM, int WN, bool GLU>
+struct Epilogue {
+  static constexpr int MI = 16;
+  static constexpr int MB = WR / MI, NB = WC / MI;
+  static constexpr int kOut = GLU ? WN * WC / 2 : WN * WC;
+  static constexpr int kLds = WM * WN * WC * 128;
+  static constexpr int UN = 16 / sizeof(O);   // values of a 16-byte piece
+  __device__ __forceinline__ static uint32_t epi_off(int r, int c) {   // c: 16-byte chunk
+    if constexpr (WC % 64 == 0) return r * WC * 4 + ((c ^ (r & 15)) << 4);
+    else return r * WC * 4 + ((c ^ ((r >> 1) & 7)) << 4);
+  }
+  __device__ __forceinline__ static void read_vals(uint32_t base, int r, int col, float (&v)[UN]) {
+#pragma unroll
+    for (int h = 0; h < UN / 4; ++h) {
+      const vec4u w = read_lds16(base + epi_off(r, col / 4 + h));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * h + i] = __uint_as_float(w[i]);
+    }
+  }
+
+  // lds: address of the staging of all waves
+  __device__ __forceinline__ static void run(const ForwardArgs& args, const TileAt& at,
+                                             const f32x4 (&acc)[MB][NB], uint32_t lds, int lane,
+                                             int wave) {
+    const int wm = wave / WN, wn = wave % WN;
+    const int F = GLU ? args.d_out / 2 : args.d_out;
+    constexpr int wave_cols = GLU ? WC / 2 : WC;
+    constexpr int lanes = wave_cols / UN;    // lanes of one row
+    constexpr int per = 64 / lanes;          // rows of one pass
+    const uint32_t base = lds + wave * WC * 128;
+    const int c = (lane % lanes) * UN;
+    const int col = at.col * kOut + wn * wave_cols + c;
+    const bool col_ok = col < F;
+    const O* bias = static_cast<const O*>(args.bias);
+    float ba[UN], bb[UN];
+#pragma unroll
+    for (int i = 0; i < UN; ++i) ba[i] = bb[i] = 0.f;
+    if (bias != nullptr && col_ok) {
+      load_vals(bias + (int64_t)at.e * args.d_out + col, ba);
+      if (GLU) load_vals(bias + (int64_t)at.e * args.d_out + F + col, bb);
+    }
+    constexpr int G = 32 / MI;   // blocks of 32 rows
+    static_for<MB / G>([&](auto a_) __attribute__((always_inline)) {
+      constexpr int a = a_ * G;
+      const int r0 = wm * WR + a * MI;
+      if (r0 < at.rows) {   // wave-uniform
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)   // a lane holds 4 columns of one row
+            *reinterpret_cast<LDS_AS f32x4*>((LDS_AS char*)(uintptr_t)(
+                base + epi_off(g * MI + lane % MI, b * (MI / 4) + lane / 16))) = acc[a + g][b];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        for (int p = 0; p < 32 / per; ++p) {
+          const int r = p * per + lane / lanes;
+          if (r0 + r < at.rows && col_ok) {
+            const int64_t o = (at.lo + r0 + r) * F + col;
+            float z[UN], v[UN];
+            read_vals(base, r, c, z);
+#pragma unroll
+            for (int i = 0; i < UN; ++i) z[i] += ba[i];
+            if (args.pre_a != nullptr) store_vals(static_cast<O*>(args.pre_a) + o, z);
+            if constexpr (GLU) {
+              float w[UN];
+              read_vals(base, r, WC / 2 + c, w);
+#pragma unroll
+              for (int i = 0; i < UN; ++i) w[i] += bb[i];
+              if (args.pre_b != nullptr) store_vals(static_cast<O*>(args.pre_b) + o, w);
+#pragma unroll
+              for (int i = 0; i < UN; ++i) v[i] = z[i] * sigmoid_f32(z[i]) * w[i];
+            } else {
+#pragma unroll
+              for (int i = 0; i < UN; ++i) v[i] = z[i];
+              activate(args.act, v);
+            }
+            if (args.residual != nullptr) {
+              float r8[UN];
+              load_vals(static_cast<const O*>(args.residual) + o, r8);
+#pragma unroll
+              for (int i = 0; i < UN; ++i) v[i] += r8[i];
+            }
+            store_vals(static_cast<O*>(args.y) + o, v);
+          }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+      }
+    });
+  }
+};
+
 // T: storage.  A wave computes WR x WC, WM x WN waves a workgroup, NS LDS
 // stages of one K step (128 bytes of every row) each.  128 bytes are a cache
 // line: 64-byte steps with twice the stages were 5 to 15 % slower on every shape,

@@ -17,6 +17,17 @@
 // float32.  Over a row that is some 2^-16 of the sum of absolute terms, far below the
 // rounding to bfloat16 at the end; exact products would take the bfloat16
 // instructions, at half the rate.
+//
+// What bounds it (one GPU's 16 experts, Zipf-shared pairs):
+//   many rows   8192^3 on one segment 435 us, 2.5 PFLOP/s (the library's product with
+//               one scale a tensor 349 us): of 820 thousand cycles the matrix units are busy
+//               in 524, a step of the loop loses some 15 % to LDS reads and loads at once,
+//               a tile about 13 us ahead of the loop and behind it.  32768 pairs, 2048 ->
+//               1536 SwiGLU with pre-activations 148 us (151 MB of rows to write), 1536 ->
+//               2048 in the gradient's direction 156 us: 16 and 12 steps a tile
+//   some rows   reading W: 512 pairs over 184 MB of W 39 us, 4.7 TB/s; 1999 pairs with one
+//               expert of 591 rows 68 us, whose tiles walk the same K with more to multiply
+//   few rows    32 pairs over 50 MB of W 12.3 us, one row 5.2 us: a walk over K
 #include "fp8.h"
 #include "grouped_tiles.h"
 
@@ -53,8 +64,9 @@ __device__ __forceinline__ f32x4 mfma(const Frag& a, const Frag& b, f32x4 c, uin
 __device__ __forceinline__ int scale_blocks(int d) { return (d + kFp8Block - 1) / kFp8Block; }
 
 // Each column tile of each expert starts its K loop this many K steps after its
-// neighbour's and goes round, so that they do not all read the same few memory channels;
-// not with 256-row tiles, which share their rows of x in the L2.
+// neighbour's and goes round, so that they do not all read the same few memory channels
+// (128 pairs over 16 x 2816 x 4096: 37.6 us, 43.6 without); not with 256-row tiles, which
+// share their rows of x in the L2 (32768 pairs, 2048 -> 1536: 145 us, 153 with).
 constexpr int kStagger = 3;
 
 // Byte q of four dwords into dword q, byte by byte (a 4 x 4 transpose).
@@ -90,7 +102,6 @@ struct Gemm8 {
   static constexpr int kMB = MB, kNB = NB;
   static constexpr int kWaves = WM * WN;
   static constexpr int kThreads = 64 * kWaves;
-  static constexpr int kWavesPerSimd = WR * WC > 64 * 128 ? 1 : 2;
   static constexpr int TM = WM * WR, TN = WN * WC;
   static constexpr int kOut = GLU ? TN / 2 : TN;
   static constexpr int kChunks = RB / 16;
@@ -104,6 +115,7 @@ struct Gemm8 {
   static constexpr int kScaleSteps = TM < 256 ? 32 : 64;
   static constexpr int kLds = NS * kStage + kScaleSteps * kUnits * 4;
   static_assert(kLds <= 160 * 1024, "LDS of a CU");
+  static constexpr int kWavesPerSimd = std::max(1, 160 * 1024 / kLds * kWaves / 4);
   static_assert(TM * RB % (1024 * kWaves) == 0 && TN * RB % (1024 * kWaves) == 0, "whole loads");
   static_assert(MB % 2 == 0 && NB % 2 == 0, "halves");
 
@@ -516,6 +528,9 @@ __global__ __launch_bounds__(G::kThreads, G::kWavesPerSimd) void gemm8_kernel(Fp
   run_tile<G>(args, at, (LDS_AS char*)smem);
 }
 
+// Tiles of 256 x 256 in four waves, one a SIMD: a wave of 128 x 128 reads half as much
+// LDS as two of 64 x 128 do (8192^3: 435 us, 440 with eight waves; 32768 pairs, 2048 ->
+// 1536: 148 and 158 us, 4096 -> 2816: 407 and 421 us).
 template <bool GLU>
 struct Ragged8 {
   typedef Gemm8<128, 128, 2, 2, 2, GLU> G256;
@@ -653,11 +668,22 @@ hipError_t launch_few_rows(const Fp8Args& a, int F, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The smallest tiles whose workgroups the CUs hold at once, as for bfloat16: below
+// that a product takes the time of one workgroup's walk over K, which grows with the
+// tile.  Measured (us; columns: without tiles, 32 x 64, 64 x 64, 64 x 128, 128 x 256,
+// and 32 x 256 for few rows of much W):
+//   1 row, 1 x 1536 x 2048 SwiGLU             5.3   8.8   8.3  10.1  18.0
+//   64 rows, 1 x 4096 x 4096                 15.8  14.4  14.0  17.4  32.5
+//   256 rows, 4 x 1536 x 2048 SwiGLU         12.0   9.7   9.5  11.5  21.0
+//   2048 rows, 4 x 1536 x 2048 SwiGLU        74    28.9  19.5  16.4  22.2
+//   8192 rows, 16 x 1536 x 2048 SwiGLU      275   108    63.5  49.5  45.9  (256 rows: 36.8)
+//   512 rows, 16 x 2816 x 4096 SwiGLU        82    45.6  50.5  45.1  43.1  (32 x 256: 39.1)
+//   128 rows, 16 x 2816 x 4096 SwiGLU        41.7  44.6  45.6  41.7  40.4  (32 x 256: 37.8)
 template <bool GLU>
 hipError_t forward(const Fp8Args& a, int F, bool far, hipStream_t s) {
   constexpr int h = GLU ? 2 : 1;   // W rows of an output column
   if (expected(a.f, F, 16, 32 / h) <= 320) return launch_few_rows<2, GLU>(a, F, s);
-  if (far) return launch_gemm<Gemm8<32, 64, 2, 2, 3, GLU, true>>(a, F, s);
+  if (far) return launch_gemm<Gemm8<32, 64, 2, 2, 3, GLU, true>>(a, F, s);   // 64-bit addresses
   if (a.f.P <= (int64_t)32 * a.f.E && expected(a.f, F, 32, 256 / h) >= 160)
     return launch_gemm<Gemm8<32, 64, 1, 4, 3, GLU>>(a, F, s);
   if (expected(a.f, F, 32, 64 / h) <= 320)

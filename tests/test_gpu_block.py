@@ -360,6 +360,63 @@ def test_product_beyond_a_buffer():
     assert bool(((got - z).abs() <= 2 * e + 2 ** -7 * z.abs()).all())
 
 
+@pytest.mark.parametrize("tile", list(TILES))
+@pytest.mark.parametrize("name", ["none", "swiglu"])
+def test_product_at_an_eighth_of_the_capacity(tile, name):
+    """As many pair rows again seven times, behind the last segment: left as they were."""
+    seg, F = TILES[tile]
+    seg, F = [s // 8 for s in seg], F // 16 * 8 if name == "swiglu" else F
+    x, W, row, bias, _ = product_inputs(seg, 272, 2 * F if name == "swiglu" else F, 6,
+                                        spare=TILES[tile][0][-1] - seg[-1], name=name)
+    check_product(seg, x, W, row, bias, None, name, False)
+
+
+def test_product_many_experts():
+    """256 experts, most of them without rows, one with most."""
+    seg = [0] * 40 + [3] * 100 + [900] * 50 + [901 + i for i in range(67)]
+    x, W, row, bias, _ = product_inputs(seg, 144, 72, 14)
+    check_product(seg, x, W, row, bias, None, "silu", True)
+
+
+def test_quantize_beyond_32_bits():
+    """Rows and weights whose elements pass 2^32: the last ones as if they were alone."""
+    D = 4096
+    T = 2 ** 32 // D + 70
+    x = torch.zeros(T, D, dtype=BF16, device=DEV)
+    tail = normal(gen(3), (70, D), BF16)
+    x[-70:] = put(tail)
+    out, ref = L.quantize_rows(x), L.quantize_rows(put(tail))
+    assert torch.equal(out["q"][-70:].view(U8), ref["q"].view(U8))
+    assert torch.equal(out["scale"][-70:], ref["scale"])
+    assert int((out["scale"][:-70] != 127).sum()) == 0
+    del out
+    W = x[: T // 128 * 128].view(1, -1, D)     # one expert's, transposed as well
+    W8 = L.quantize_weights(W, transpose=True)
+    end = W[0, -128:]
+    want = L.quantize_weights(end[None].contiguous(), transpose=True)
+    assert torch.equal(W8["q"][0, -128:].view(U8), want["q"][0].view(U8))
+    assert torch.equal(W8["scale"][0, -1], want["scale"][0, 0])
+    assert torch.equal(W8["qt"][0, :, -128:].contiguous().view(U8), want["qt"][0].view(U8))
+    last = W.shape[1] // 128 - 1
+    assert torch.equal(W8["scale_t"][0, :, last], want["scale_t"][0, :, 0])
+
+
+def test_results_into_given_buffers():
+    """out's buffers are the results, and nothing beside them is written."""
+    x = put(normal(gen(5), (33, 272), BF16))
+    ref = L.quantize_rows(x)
+    q, s = torch.full((35, 272), 9, dtype=U8, device=DEV), torch.full((35, 4), 9, dtype=U8, device=DEV)
+    out = dict(q=q[1:34].view(L.FP8), scale=s[1:34])
+    with pytest.raises(L.LrmoeError):          # a row of scales is no 16-byte border
+        L.quantize_rows(x, out=out)
+    q, s = torch.full((48, 272), 9, dtype=U8, device=DEV), torch.full((48, 4), 9, dtype=U8, device=DEV)
+    out = dict(q=q[4:37].view(L.FP8), scale=s[4:37])
+    assert L.quantize_rows(x, out=out) is out
+    assert torch.equal(q[4:37], ref["q"].view(U8)) and torch.equal(s[4:37], ref["scale"])
+    assert bool((q[:4] == 9).all() and (q[37:] == 9).all() and (s[:4] == 9).all()
+                and (s[37:] == 9).all())
+
+
 # ------------------------------------------------------------------- norms
 
 NORMS = [(1, 8), (3, 64), (5, 520), (33, 512), (130, 1032), (9, 2048), (6, 2056), (1100, 136),
