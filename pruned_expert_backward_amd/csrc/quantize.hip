@@ -66,8 +66,9 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const T* x, int64_t 
 }
 
 // ---- weights: a workgroup a block, a patch of 8 x 8 a thread
-constexpr int kPitch = kFp8Block + 8;   // LDS row of the transposed block: 8-byte patches
-                                        // of 16 rows fall on distinct banks
+// LDS row of the transposed block.  Four of sixteen patches share a bank; that hides
+// behind the memory traffic (the kernel takes 40.7 us where a copy would take 39).
+constexpr int kPitch = kFp8Block + 8;
 
 template <typename T>
 __global__ __launch_bounds__(256) void quantize_weights_kernel(const T* W, int N, int K,
