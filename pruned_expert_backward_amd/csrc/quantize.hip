@@ -9,6 +9,8 @@
 // Memory bound: every value is read once and written once (twice with the
 // transpose), 2 or 4 bytes in and 1 out.  8191 x 4096 float32 rows (168 MB) 32.5 us,
 // 5.2 TB/s; 16 x 1536 x 2048 bfloat16 weights in both orders (201 MB) 44 us, 4.5 TB/s.
+#include <algorithm>
+
 #include "forward.h"
 #include "fp8.h"
 
@@ -136,11 +138,20 @@ template <typename T>
 hipError_t quantize_rows(const void* x, int64_t rows, int D, uint8_t* q, uint8_t* scale,
                          hipStream_t s) {
   const int blocks = (D + kFp8Block - 1) / kFp8Block;
-  const int64_t groups = (rows * blocks + kPerGroup - 1) / kPerGroup;
-  if (groups * 256 >= int64_t(1) << 32) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(quantize_rows_kernel<T>, dim3((uint32_t)groups), dim3(256), 0, s,
-                     static_cast<const T*>(x), rows, D, blocks, fp8_scale_row(D), q, scale);
-  return hipGetLastError();
+  // a grid has less than 2^32 threads: 2^30 blocks and more take several launches, of
+  // whole rows each
+  const int64_t most = ((int64_t(1) << 24) - 1) * kPerGroup / blocks;
+  const int pitch = fp8_scale_row(D);
+  for (int64_t r = 0; r < rows; r += most) {
+    const int64_t n = std::min(most, rows - r);
+    hipLaunchKernelGGL(quantize_rows_kernel<T>,
+                       dim3((uint32_t)((n * blocks + kPerGroup - 1) / kPerGroup)), dim3(256), 0, s,
+                       static_cast<const T*>(x) + r * D, n, D, blocks, pitch, q + r * D,
+                       scale + r * pitch);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
