@@ -435,7 +435,7 @@ __global__ __launch_bounds__(512, 2) void ragged_gemm_kernel(ForwardArgs args, i
   typedef Ragged<T, GLU> R;
   __shared__ __attribute__((aligned(16))) char smem[R::kLds];
   TileAt at;
-  if (!find_ragged_tile(args.seg, args.E, args.P, cols, blockIdx.x, at) || at.rows <= 0) return;
+  if (!find_ragged_tile(args.seg, args.E, args.P, cols, at)) return;
   if (at.rows > 128) run_tile<typename R::G256>(args, at, (LDS_AS char*)smem);
   else if (at.rows > 64) run_tile<typename R::G128>(args, at, (LDS_AS char*)smem);
   else run_tile<typename R::G64>(args, at, (LDS_AS char*)smem);

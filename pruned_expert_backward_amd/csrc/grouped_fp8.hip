@@ -545,8 +545,7 @@ __global__ __launch_bounds__(256, 1) void ragged_gemm8_kernel(Fp8Args args, int 
   typedef Ragged8<GLU> R;
   __shared__ __attribute__((aligned(16))) char smem[R::kLds];
   TileAt at;
-  if (!find_ragged_tile(args.f.seg, args.f.E, args.f.P, cols, blockIdx.x, at) || at.rows <= 0)
-    return;
+  if (!find_ragged_tile(args.f.seg, args.f.E, args.f.P, cols, at)) return;
   if (at.rows > 128) run_tile<typename R::G256>(args, at, (LDS_AS char*)smem);
   else if (at.rows > 64) run_tile<typename R::G128>(args, at, (LDS_AS char*)smem);
   else run_tile<typename R::G64>(args, at, (LDS_AS char*)smem);

@@ -106,10 +106,10 @@ __device__ __forceinline__ bool find_tile(const int32_t* seg, int E, int64_t P, 
 
 constexpr int kXcds = 8, kXcdCus = 32;
 
-// Tile of workgroup `block` of the launch, false behind the last one.  A piece of a cut
-// tile may have no rows.
+// Tile of this workgroup, or false (behind the last one, or a piece of a cut tile
+// without rows).
 __device__ __forceinline__ bool find_ragged_tile(const int32_t* seg, int E, int64_t P, int cols,
-                                                 int64_t block, TileAt& at) {
+                                                 TileAt& at) {
   const int lane = threadIdx.x & 63;
   int64_t off[5];
 #pragma unroll
@@ -137,8 +137,8 @@ __device__ __forceinline__ bool find_ragged_tile(const int32_t* seg, int E, int6
   const int fend = wave_scan(full), pend = wave_scan(part);
   const int fulls = __builtin_amdgcn_readlane(fend, 63);
   const int parts = __builtin_amdgcn_readlane(pend, 63);
-  const int x = block % kXcds;
-  const int64_t pos = block / kXcds;
+  const int x = blockIdx.x % kXcds;
+  const int64_t pos = blockIdx.x / kXcds;
   const int64_t ft = (int64_t)fulls * cols, pt = (int64_t)parts * cols;
   const int64_t f0 = ft * x / kXcds, f1 = ft * (x + 1) / kXcds;   // this XCD's share
   const int64_t p0 = pt * x / kXcds, p1 = pt * (x + 1) / kXcds;
@@ -170,8 +170,7 @@ __device__ __forceinline__ bool find_ragged_tile(const int32_t* seg, int E, int6
   r = __builtin_amdgcn_readfirstlane(r);
   at.col = __builtin_amdgcn_readfirstlane(at.col);
   const unsigned long long past = whole ? __ballot(fend > r) : __ballot(pend > r);
-  at.rows = 0;
-  if (past == 0) return true;   // offsets out of order
+  if (past == 0) return false;   // offsets out of order
   const int owner = __ffsll(past) - 1;
   int sub = whole ? r - (fend - full) : r - (pend - part), j = 0;   // meant for the owner lane
   const bool sane = sub >= 0;
@@ -192,7 +191,7 @@ __device__ __forceinline__ bool find_ragged_tile(const int32_t* seg, int E, int6
   at.e = __builtin_amdgcn_readlane(4 * lane + j, owner);
   at.lo = (uint32_t)__builtin_amdgcn_readlane((uint32_t)(oj + first), owner);   // P < 2^31
   at.rows = __builtin_amdgcn_readlane(rows, owner);
-  return true;
+  return at.rows > 0;
 }
 
 // ---- global -> LDS, 16 bytes a lane: lane i writes LDS bytes [lds + 16 i,
