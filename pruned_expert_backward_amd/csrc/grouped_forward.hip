@@ -533,9 +533,7 @@ template <typename G>
 hipError_t launch_gemm(const ForwardArgs& a, int F, hipStream_t s) {
   const int cols = (F + G::kOut - 1) / G::kOut;
   const int64_t blocks = grid_blocks(a.P, a.E, G::TM, cols);
-  if (blocks * G::kThreads >= int64_t(1) << 32) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(gemm_kernel<G>, dim3((uint32_t)blocks), dim3(G::kThreads), 0, s, a, cols);
-  return hipGetLastError();
+  return launch_workgroups(gemm_kernel<G>, blocks, G::kThreads, s, a, cols);
 }
 
 template <typename T, bool GLU>
@@ -543,10 +541,7 @@ hipError_t launch_ragged(const ForwardArgs& a, int F, hipStream_t s) {
   typedef Ragged<T, GLU> R;
   const int cols = (F + R::kOut - 1) / R::kOut;
   const int64_t blocks = ragged_blocks(a, cols);
-  if (blocks * R::kThreads >= int64_t(1) << 32) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((ragged_gemm_kernel<T, GLU>), dim3((uint32_t)blocks), dim3(R::kThreads), 0, s,
-                     a, cols);
-  return hipGetLastError();
+  return launch_workgroups(ragged_gemm_kernel<T, GLU>, blocks, R::kThreads, s, a, cols);
 }
 
 template <typename T, int NC, bool GLU>
@@ -554,10 +549,7 @@ hipError_t launch_few_rows(const ForwardArgs& a, int F, hipStream_t s) {
   constexpr int kOut = GLU ? NC * 8 : NC * 16;
   const int cols = (F + kOut - 1) / kOut;
   const int64_t blocks = grid_blocks(a.P, a.E, 16, cols);
-  if (blocks * 256 >= int64_t(1) << 32) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((few_rows_kernel<T, NC, GLU>), dim3((uint32_t)blocks), dim3(256), 0, s, a,
-                     cols);
-  return hipGetLastError();
+  return launch_workgroups(few_rows_kernel<T, NC, GLU>, blocks, 256, s, a, cols);
 }
 
 // The smallest tiles whose workgroups the 256 CUs hold at once, or nearly:

@@ -640,9 +640,7 @@ template <typename G>
 hipError_t launch_gemm(const Fp8Args& a, int F, hipStream_t s) {
   const int cols = (F + G::kOut - 1) / G::kOut;
   const int64_t blocks = grid_blocks(a.f.P, a.f.E, G::TM, cols);
-  if (blocks * G::kThreads >= int64_t(1) << 32) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(gemm8_kernel<G>, dim3((uint32_t)blocks), dim3(G::kThreads), 0, s, a, cols);
-  return hipGetLastError();
+  return launch_workgroups(gemm8_kernel<G>, blocks, G::kThreads, s, a, cols);
 }
 
 template <bool GLU>
@@ -650,10 +648,7 @@ hipError_t launch_ragged(const Fp8Args& a, int F, hipStream_t s) {
   typedef Ragged8<GLU> R;
   const int cols = (F + R::kOut - 1) / R::kOut;
   const int64_t blocks = ragged_blocks(a.f, cols);
-  if (blocks * R::kThreads >= int64_t(1) << 32) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((ragged_gemm8_kernel<GLU>), dim3((uint32_t)blocks), dim3(R::kThreads), 0, s,
-                     a, cols);
-  return hipGetLastError();
+  return launch_workgroups(ragged_gemm8_kernel<GLU>, blocks, R::kThreads, s, a, cols);
 }
 
 template <int NC, bool GLU>
@@ -661,10 +656,7 @@ hipError_t launch_few_rows(const Fp8Args& a, int F, hipStream_t s) {
   constexpr int kOut = GLU ? NC * 8 : NC * 16;
   const int cols = (F + kOut - 1) / kOut;
   const int64_t blocks = grid_blocks(a.f.P, a.f.E, 16, cols);
-  if (blocks * 256 >= int64_t(1) << 32) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((few_rows8_kernel<NC, GLU>), dim3((uint32_t)blocks), dim3(256), 0, s, a,
-                     cols);
-  return hipGetLastError();
+  return launch_workgroups(few_rows8_kernel<NC, GLU>, blocks, 256, s, a, cols);
 }
 
 // The smallest tiles whose workgroups the CUs hold at once, as for bfloat16: below

@@ -49,6 +49,13 @@ struct TileAt {
   int col;       // column tile
 };
 
+// A launch of any number of workgroups: a dimension of a grid has less than 2^32
+// threads, so its workgroups go by rows of 2^22 (whole turns of the XCDs).
+constexpr int kGridRow = 22;
+__device__ __forceinline__ int64_t workgroup() {
+  return (int64_t)blockIdx.y << kGridRow | blockIdx.x;
+}
+
 // Tile of this workgroup, or false.  Workgroup b runs on XCD b % 8, so each
 // XCD takes a contiguous eighth of the tiles; inside it, kGroup row tiles go
 // column by column.  Each wave finds the tile for itself: lane l counts the
@@ -73,8 +80,9 @@ __device__ __forceinline__ bool find_tile(const int32_t* seg, int E, int64_t P, 
   const int all = __builtin_amdgcn_readlane(end, 63);
   const int64_t total = (int64_t)all * cols;
   const int64_t share = (total + 7) / 8;
-  const int64_t t = (int64_t)(blockIdx.x & 7) * share + (blockIdx.x >> 3);
-  if ((int64_t)(blockIdx.x >> 3) >= share || t >= total) return false;
+  const int64_t block = workgroup();
+  const int64_t t = (block & 7) * share + (block >> 3);
+  if ((block >> 3) >= share || t >= total) return false;
   const int64_t per = (int64_t)kGroup * cols;
   const int g = (int)(t / per);
   const int in = (int)(t - g * per);
@@ -137,8 +145,9 @@ __device__ __forceinline__ bool find_ragged_tile(const int32_t* seg, int E, int6
   const int fend = wave_scan(full), pend = wave_scan(part);
   const int fulls = __builtin_amdgcn_readlane(fend, 63);
   const int parts = __builtin_amdgcn_readlane(pend, 63);
-  const int x = blockIdx.x % kXcds;
-  const int64_t pos = blockIdx.x / kXcds;
+  const int64_t block = workgroup();
+  const int x = block % kXcds;
+  const int64_t pos = block / kXcds;
   const int64_t ft = (int64_t)fulls * cols, pt = (int64_t)parts * cols;
   const int64_t f0 = ft * x / kXcds, f1 = ft * (x + 1) / kXcds;   // this XCD's share
   const int64_t p0 = pt * x / kXcds, p1 = pt * (x + 1) / kXcds;
@@ -282,6 +291,17 @@ __device__ __forceinline__ void few_rows_epilogue(const ForwardArgs& args, const
 }
 
 // ---------------------------------------------------------------- launch
+// `kernel` in as many workgroups.
+template <typename... A>
+hipError_t launch_workgroups(void (*kernel)(A...), int64_t blocks, int threads, hipStream_t s,
+                             const A&... args) {
+  const int64_t row = int64_t(1) << kGridRow, rows = (blocks + row - 1) / row;
+  if (rows > 65535) return hipErrorInvalidValue;   // 2^38 workgroups: no memory holds their rows
+  hipLaunchKernelGGL(kernel, dim3((uint32_t)std::min(blocks, row), (uint32_t)rows), dim3(threads),
+                     0, s, args...);
+  return hipGetLastError();
+}
+
 int64_t grid_blocks(int64_t P, int E, int tm, int64_t cols) {
   const int64_t tiles = P / tm + (P < E ? P : E);   // most row tiles of P rows over E experts
   return (tiles * cols + 7) / 8 * 8;
