@@ -732,6 +732,13 @@ lrmoe_status lrmoe_residual_norm_backward(const lrmoe_norm* nm, const void* ds, 
  * and bfloat16 parameters are rounded stochastically: up with a probability of
  * the distance from the lower neighbour (in 65536ths), so that small changes are
  * not lost on average; a second moment that is not zero is not rounded to zero.
+ * So m and the root keep their means, and v, the root's square, gains the rounding's
+ * variance: it is 2.6 % (beta2 0.95) to 4.3 % (0.999) high on average where the root is
+ * within 2^-14 of its block's largest, and nine in ten elements are between 0.65 and 1.6
+ * times the exact v at any one step.  From 2^-16 to 2^-18 of the largest, v is 1.8 to 1.9
+ * times the exact one, and a root further below is held at the smallest code, 2^-9 of the
+ * scale: those elements take smaller steps.  Tensors whose neighbouring elements' gradients
+ * differ by more than that want float32 states.
  * The random bits of element i of tensor k are a hash of (seed, step, k, i):
  *   mix(a): a ^= a >> 16; a *= 0x6A09E667; a ^= a >> 15; a *= 0xBB67AE85;
  *           a ^= a >> 16                                        (32 bits)

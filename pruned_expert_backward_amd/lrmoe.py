@@ -1190,7 +1190,8 @@ def residual_norm_backward(s, ds=None, dh=None, y=None, weight=None, branch_weig
 def adamw_state(param, bits: int = 32) -> dict:
     """Zero moments of a parameter: float32 m and v, or 8-bit (float8_e4m3fn) m and
     root (the root of the second moment) with m_scale and root_scale, uint8, a byte for each
-    run of 128 elements."""
+    run of 128 elements.  A root less than 2^-17 of its run's largest is held at the smallest
+    code, so such elements take smaller steps: 32 bits for tensors of which that matters."""
     n, dev = param.numel(), param.device
     if bits == 32:
         return dict(m=torch.zeros(n, dtype=torch.float32, device=dev),
