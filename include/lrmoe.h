@@ -749,7 +749,7 @@ lrmoe_status lrmoe_residual_norm_backward(const lrmoe_norm* nm, const void* ds, 
  * ------------------------------------------------------------------------ */
 
 typedef struct {
-  int64_t n;         /* elements (0: skipped)                                */
+  int64_t n;         /* elements, 0 <= n < 2^36 (0: skipped)                 */
   void* p;           /* parameter [n], updated                               */
   const void* g;     /* gradient [n]                                         */
   void* m;           /* first moment [n], updated                            */

@@ -320,6 +320,7 @@ hipError_t launch_adamw(const lrmoe_adamw* c, const lrmoe_adamw_tensor* t, int32
     int64_t blocks = 0;
     for (int32_t k = 0; k <= count; ++k) {
       const bool full = st.count == kMost;
+      // at most 2^23: a tensor has less than 2^36 elements
       const int64_t need = k < count ? (t[k].n + st.chunk - 1) / st.chunk : 0;
       if (st.count > 0 && (k == count || full || blocks + need >= int64_t(1) << 24)) {
         const hipError_t e = kLaunch[p][g][b](a, (uint32_t)blocks, s);
@@ -331,7 +332,6 @@ hipError_t launch_adamw(const lrmoe_adamw* c, const lrmoe_adamw_tensor* t, int32
       if ((t[k].p_dtype == LRMOE_BF16) != (p != 0) || (t[k].g_dtype == LRMOE_BF16) != (g != 0) ||
           (t[k].m_scale != nullptr) != (b != 0) || t[k].n == 0)
         continue;
-      if (need >= int64_t(1) << 24) return hipErrorInvalidValue;
       a.t[st.count] = Tensor{t[k].p, t[k].g, t[k].m, t[k].v, t[k].m_scale, t[k].v_scale,
                              static_cast<uint16_t*>(t[k].copy), t[k].n};
       a.first[st.count] = (uint32_t)blocks;

@@ -8,6 +8,8 @@ using namespace lrmoe;
 
 namespace {
 
+constexpr int64_t kMaxElements = int64_t(1) << 36;   // of a tensor of the optimizer's step
+
 lrmoe_status check_rows(int64_t T) { return T < 0 || T >= kMaxRows ? LRMOE_ERR_SHAPE : LRMOE_OK; }
 
 // A row length in 8 bits: whole 16-byte pieces.
@@ -190,7 +192,7 @@ lrmoe_status lrmoe_adamw_step(const lrmoe_adamw* cfg, const lrmoe_adamw_tensor* 
     return LRMOE_ERR_ALIGN;
   for (int32_t k = 0; k < count; ++k) {
     const lrmoe_adamw_tensor& t = tensors[k];
-    if (t.n < 0) return LRMOE_ERR_SHAPE;
+    if (t.n < 0 || t.n >= kMaxElements) return LRMOE_ERR_SHAPE;
     LRMOE_TRY(check_dtype(t.p_dtype));
     LRMOE_TRY(check_dtype(t.g_dtype));
     LRMOE_TRY(need(t.p, t.n));
