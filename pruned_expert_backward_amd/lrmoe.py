@@ -1227,7 +1227,8 @@ def adamw_step(params: Sequence, grads: Sequence, states: Sequence, step, lr,
     and lr are numbers, or one-element device tensors (int64, float32) that a captured
     call reads at each replay.  grad_scale (float32 tensor) multiplies the gradients;
     nothing is changed where skip (float32 tensor) is not 0.  seed: of the stochastic
-    rounding of 8-bit states and bfloat16 parameters; the step enters by itself."""
+    rounding of 8-bit states and bfloat16 parameters; the step enters by itself.  What is
+    updated must not overlap: all tensors are worked on at once."""
     count = len(params)
     if len(grads) != count or len(states) != count or (copies is not None and
                                                        len(copies) != count):
@@ -1267,6 +1268,11 @@ def adamw_step(params: Sequence, grads: Sequence, states: Sequence, step, lr,
             moments = flat("m", st["m"], f32, n), flat("v", st["v"], f32, n), 0, 0
         rows += (n, like("params", p, pd, shape), like("grads", g, gd, shape), *moments,
                  0 if copy is None else like("copies", copy, bf16, shape), pt | gt << 32)
+    for name, field in (("params", 1), ("states", 3)):   # p and m of the descriptors
+        if len(set(rows[field::9])) < count:             # (empty tensors have the same address)
+            live = [rows[i + field] for i in range(0, len(rows), 9) if rows[i]]
+            if len(set(live)) < len(live):
+                raise ValueError(f"{name}: a tensor is there twice, and would be updated at once")
     host = array.array("q", rows)
     table = (AdamWTensor * count).from_buffer(host)
     on_dev = isinstance(step, torch.Tensor), isinstance(lr, torch.Tensor)
