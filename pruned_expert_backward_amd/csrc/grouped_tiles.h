@@ -49,11 +49,14 @@ struct TileAt {
   int col;       // column tile
 };
 
+constexpr int kXcds = 8, kXcdCus = 32;
+
 // A launch of any number of workgroups: a dimension of a grid has less than 2^32
-// threads, so its workgroups go by rows of 2^22 (whole turns of the XCDs).
-constexpr int kGridRow = 22;
-__device__ __forceinline__ int64_t workgroup() {
-  return (int64_t)blockIdx.y << kGridRow | blockIdx.x;
+// threads, so its workgroups go by rows of 2^22, whole turns of the XCDs.  This
+// workgroup's number among those of its XCD, which is blockIdx.x % kXcds.
+constexpr int kGridRow = 22, kGridRows = 1 << 13;   // numbers of 32 bits
+__device__ __forceinline__ uint32_t number_on_xcd() {
+  return blockIdx.y * ((1u << kGridRow) / kXcds) + blockIdx.x / kXcds;
 }
 
 // Tile of this workgroup, or false.  Workgroup b runs on XCD b % 8, so each
@@ -80,9 +83,9 @@ __device__ __forceinline__ bool find_tile(const int32_t* seg, int E, int64_t P, 
   const int all = __builtin_amdgcn_readlane(end, 63);
   const int64_t total = (int64_t)all * cols;
   const int64_t share = (total + 7) / 8;
-  const int64_t block = workgroup();
-  const int64_t t = (block & 7) * share + (block >> 3);
-  if ((block >> 3) >= share || t >= total) return false;
+  const int64_t pos = number_on_xcd();
+  const int64_t t = (int64_t)(blockIdx.x % kXcds) * share + pos;
+  if (pos >= share || t >= total) return false;
   const int64_t per = (int64_t)kGroup * cols;
   const int g = (int)(t / per);
   const int in = (int)(t - g * per);
@@ -111,8 +114,6 @@ __device__ __forceinline__ bool find_tile(const int32_t* seg, int E, int64_t P, 
   at.rows = __builtin_amdgcn_readlane(rows, owner);
   return at.rows > 0;
 }
-
-constexpr int kXcds = 8, kXcdCus = 32;
 
 // Tile of this workgroup, or false (behind the last one, or a piece of a cut tile
 // without rows).
@@ -145,9 +146,8 @@ __device__ __forceinline__ bool find_ragged_tile(const int32_t* seg, int E, int6
   const int fend = wave_scan(full), pend = wave_scan(part);
   const int fulls = __builtin_amdgcn_readlane(fend, 63);
   const int parts = __builtin_amdgcn_readlane(pend, 63);
-  const int64_t block = workgroup();
-  const int x = block % kXcds;
-  const int64_t pos = block / kXcds;
+  const int x = blockIdx.x % kXcds;
+  const int64_t pos = number_on_xcd();
   const int64_t ft = (int64_t)fulls * cols, pt = (int64_t)parts * cols;
   const int64_t f0 = ft * x / kXcds, f1 = ft * (x + 1) / kXcds;   // this XCD's share
   const int64_t p0 = pt * x / kXcds, p1 = pt * (x + 1) / kXcds;
@@ -296,7 +296,7 @@ template <typename... A>
 hipError_t launch_workgroups(void (*kernel)(A...), int64_t blocks, int threads, hipStream_t s,
                              const A&... args) {
   const int64_t row = int64_t(1) << kGridRow, rows = (blocks + row - 1) / row;
-  if (rows > 65535) return hipErrorInvalidValue;   // 2^38 workgroups: no memory holds their rows
+  if (rows > kGridRows) return hipErrorInvalidValue;   // 2^35: no memory holds their tiles
   hipLaunchKernelGGL(kernel, dim3((uint32_t)std::min(blocks, row), (uint32_t)rows), dim3(threads),
                      0, s, args...);
   return hipGetLastError();
