@@ -626,9 +626,9 @@ lrmoe_status lrmoe_act_backward(const lrmoe_forward* fw, int32_t dz_dtype,
 /* ------------------------------------------------------------------------
  * 8-bit expert products.  Values in e4m3 (finite up to 448), one power-of-two
  * scale 2^(byte - 127) for each block of 128: the smallest one with the block's
- * largest magnitude at most 448 * scale (1 for a block of zeros).  Rows have blocks
- * of 1 x 128, weights of 128 x 128; the last block of a row, column or weight may
- * be smaller.  A row of scales has ceil(columns / 128) bytes, padded with 127
+ * largest magnitude at most 448 * scale, from 2^-126 on (1 for a block of zeros).
+ * Rows have blocks of 1 x 128, weights of 128 x 128; the last block of a row, column or
+ * weight may be smaller.  A row of scales has ceil(columns / 128) bytes, padded with 127
  * to a multiple of four:
  *   S(d) = 4 * ceil(ceil(d / 128) / 4)
  * Infinity and NaN become the NaN code and do not count in their block's scale.
@@ -677,7 +677,9 @@ lrmoe_status lrmoe_grouped_forward_quantized(const lrmoe_forward* fw, const int3
  * rounding; each output is rounded once.
  * ------------------------------------------------------------------------ */
 
-#define LRMOE_MAX_NORM_WIDTH 16384 /* columns of a row */
+/* columns of a row; the gradient of more than 8192 takes 3.5 to 4.3 times as long as its
+ * bytes */
+#define LRMOE_MAX_NORM_WIDTH 16384
 
 typedef enum {
   LRMOE_BRANCH_GATE_NONE = 0,    /* 1                                        */

@@ -11,13 +11,20 @@
 //   dw  = sum over rows dh n,  dw_b = sum d g z,  dg = sum d b (over rows or columns)
 //
 // Memory bound: the forward reads x and y and writes s and h, the gradient
-// reads ds, dh, s and y and writes dx and dy; everything between stays in registers.
+// reads ds, dh, s and y and writes dx and dy.
 // A row belongs to WPR waves; each lane holds PIECES 16-byte pieces of it and of the
 // weights, which stay in registers over the rows that the waves go through.  The sums
-// over rows stay in registers too; every group of waves leaves its own in the
+// over rows stay with the lanes too; every group of waves leaves its own in the
 // workspace and a second kernel adds them in one order.  The gradient loads a row ahead.
+// All of that fits the registers in the forward, and in the gradient for rows up to
+// 8192 columns in bfloat16 and 4096 in float32.  Beyond, 16 waves a row leave a lane of the
+// gradient 128 registers, and it spills: in float32 29 of them up to 8192 columns, above
+// 8192 columns 147 in bfloat16 and 338 in float32.
 // bfloat16, TB/s: 32768 x 2048 104 us (5.2), its gradient with all sums 158 us (5.1);
-// 32768 x 4096 209 and 294 us, 8192 x 8192 102 and 167, 32768 x 512 22 and 49.
+// 32768 x 4096 209 and 294 us, 8192 x 8192 100 and 163, 32768 x 512 22 and 45.
+// float32: 32768 x 2048 209 us (5.1) and 310 (5.2), 16384 x 4096 204 and 294 (5.5).  With
+// spills: float32 8192 x 8192 203 and 367 us (4.4), 4096 x 16384 in bfloat16 101 and 669
+// (1.2), in float32 198 and 1096 us (1.5).
 // 16 rows 3.1 us, 512 rows' gradient 15.5 us: two launches and a few waits.
 #include <algorithm>
 

@@ -18,11 +18,14 @@
 // rounding to bfloat16 at the end; exact products would take the bfloat16
 // instructions, at half the rate.
 //
-// What bounds it (one GPU's 16 experts, Zipf-shared pairs):
-//   many rows   8192^3 on one segment 435 us, 2.5 PFLOP/s (the library's product with
-//               one scale a tensor 349 us): of 820 thousand cycles the matrix units are busy
-//               in 524, a step of the loop loses some 15 % to LDS reads and loads at once,
-//               a tile about 13 us ahead of the loop and behind it.  32768 pairs, 2048 ->
+// What bounds it (one GPU's 16 experts, Zipf-shared pairs; the product alone, many in a row
+// with two or three sets of inputs in turn.  Behind the quantisation of its rows, which
+// leaves them in the caches and the clock higher, the training products take 140 and 151 us):
+//   many rows   8192^3 on one segment 442 us, 2.5 PFLOP/s (the library's product with
+//               one scale a tensor 355 us): of 820 thousand cycles the matrix units are busy
+//               in 524.  A step of the loop loses some 15 % to LDS reads and loads at once
+//               (80 thousand), a tile about 13 us ahead of the loop and behind it (100
+//               thousand); the other 110 thousand are not accounted for.  32768 pairs, 2048 ->
 //               1536 SwiGLU with pre-activations 148 us (151 MB of rows to write), 1536 ->
 //               2048 in the gradient's direction 156 us: 16 and 12 steps a tile
 //   some rows   reading W: 512 pairs over 184 MB of W 39 us, 4.7 TB/s; 1999 pairs with one
@@ -529,8 +532,8 @@ __global__ __launch_bounds__(G::kThreads, G::kWavesPerSimd) void gemm8_kernel(Fp
 }
 
 // Tiles of 256 x 256 in four waves, one a SIMD: a wave of 128 x 128 reads half as much
-// LDS as two of 64 x 128 do (8192^3: 435 us, 440 with eight waves; 32768 pairs, 2048 ->
-// 1536: 148 and 158 us, 4096 -> 2816: 407 and 421 us).
+// LDS as two of 64 x 128 do (8192^3 in turns: 435 us, 440 with eight waves; 32768 pairs,
+// 2048 -> 1536: 148 and 158 us, 4096 -> 2816: 407 and 421 us).
 template <bool GLU>
 struct Ragged8 {
   typedef Gemm8<128, 128, 2, 2, 2, GLU> G256;

@@ -7,8 +7,11 @@
 //            that the forward product has read
 //
 // Memory bound: every value is read once and written once (twice with the
-// transpose), 2 or 4 bytes in and 1 out.  8191 x 4096 float32 rows (168 MB) 32.5 us,
-// 5.2 TB/s; 16 x 1536 x 2048 bfloat16 weights in both orders (201 MB) 44 us, 4.5 TB/s.
+// transpose), 2 or 4 bytes in and 1 out.  The kernels' own times: 8191 x 4096 float32
+// rows (168 MB) 30.4 us, 5.5 TB/s; 16 x 1536 x 2048 bfloat16 weights in both orders (201
+// MB) 41.1 us, 4.9 TB/s.  bfloat16 rows stay below that: 32768 x 1536 35.4 us (4.3 TB/s),
+// 8192 x 4096 27.2 (3.7), 8192 x 2048 15.2 (3.3), 501 x 4096 6.3; a lane has four 16-byte
+// loads under way where a float32 one has eight, and stores 8 bytes at a time.
 #include <algorithm>
 
 #include "forward.h"
